@@ -180,7 +180,7 @@ gemm_status_t gemm_paged_attention(gemm_handle_t h, const gemm_paged_attention_t
 gemm_status_t gemm_cache_grow(gemm_handle_t h, const gemm_cache_t* c, int64_t n, const int32_t* seqs,
                               const int32_t* counts, int64_t tokens, int64_t* positions, int64_t* slots,
                               int32_t* info, void* stream) {
-  gemm_status_t st = check_cache(h, c, n, false);
+  gemm_status_t st = check_cache(h, c, n, true);
   if (st == GEMM_OK) st = check_state(*c, true);
   if (st != GEMM_OK) return st;
   if (info == nullptr || tokens < 0 || tokens > kMaxInt || (n > 0 && (seqs == nullptr || counts == nullptr)))
@@ -190,8 +190,8 @@ gemm_status_t gemm_cache_grow(gemm_handle_t h, const gemm_cache_t* c, int64_t n,
   void* ws;
   st = scratch_of(h->cache_ws, dgt::cache_scratch_bytes(c->num_pages, n), &ws);
   if (st != GEMM_OK) return st;
-  return cuda_status(dgt::launch_cache_grow(*c, n, seqs, counts, tokens, positions, slots, info, ws, h->d_status,
-                                            static_cast<cudaStream_t>(stream)));
+  return cuda_status(dgt::launch_cache_grow(*c, n, seqs, counts, tokens, positions, slots, info, ws, h->sms,
+                                            h->d_status, static_cast<cudaStream_t>(stream)));
 }
 
 gemm_status_t gemm_cache_shrink(gemm_handle_t h, const gemm_cache_t* c, int64_t n, const int32_t* seqs,

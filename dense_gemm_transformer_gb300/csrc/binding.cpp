@@ -476,10 +476,10 @@ PyObject* pack(std::initializer_list<at::Tensor> tensors) {
   return t;
 }
 
-// handle, table, lens, refs, page_size, seqs, counts, tokens, stream
+// handle, table, lens, refs, page_size, seqs, counts, tokens, stream, pools
 PyObject* cache_grow(PyObject* const* x) {
   Device dev;
-  const gemm_cache_t c = cache_of(dev, nullptr, x[1], x[2], x[3], x[4]);
+  const gemm_cache_t c = cache_of(dev, x[9] == Py_None ? nullptr : x[9], x[1], x[2], x[3], x[4]);
   const at::Tensor& seqs = tensor(x[5], "seqs");
   const int64_t n = seqs.numel(), tokens = integer(x[7]);
   if (tokens < 0) refuse("tokens must not be negative");
@@ -572,7 +572,7 @@ PyMethodDef g_methods[] = {
     method<rotary, 11>("rotary"),
     method<rotary_append, 13>("rotary_append"),
     method<paged_attention, 15>("paged_attention"),
-    method<cache_grow, 9>("cache_grow"),
+    method<cache_grow, 10>("cache_grow"),
     method<cache_shrink, 8>("cache_shrink"),
     method<cache_fork, 9>("cache_fork"),
     method<cache_compact, 5>("cache_compact"),

@@ -245,7 +245,7 @@ cudaError_t launch_paged_attention(const gemm_paged_attention_t& a, const PagedP
 size_t cache_scratch_bytes(int64_t num_pages, int64_t n);
 cudaError_t launch_cache_grow(const gemm_cache_t& c, int64_t n, const int32_t* seqs, const int32_t* counts,
                               int64_t tokens, int64_t* positions, int64_t* slots, int32_t* info, void* scratch,
-                              int* status, cudaStream_t stream);
+                              int sms, int* status, cudaStream_t stream);
 cudaError_t launch_cache_shrink(const gemm_cache_t& c, int64_t n, const int32_t* seqs, const int32_t* counts,
                                 int* status, cudaStream_t stream);
 cudaError_t launch_cache_fork(const gemm_cache_t& c, int64_t n, const int32_t* parents, const int32_t* children,

@@ -242,8 +242,9 @@ __device__ __forceinline__ bool checked_seq(const PageState& st, int seq) {
 
 __global__ void __launch_bounds__(kIdxThreads)
     cache_grow_kernel(const PageState st, const Scratch ws, int n, const int32_t* seqs, const int32_t* counts,
-                      int tokens, int64_t* positions, int64_t* slots, int32_t* info) {
+                      int tokens, int64_t* positions, int64_t* slots, int32_t* info, int copies) {
   __shared__ IdxShared sh;
+  __shared__ int moves;
   grid_dep_wait();
   grid_dep_launch();
   if (!list_pages(st, ws, sh, false)) return;
@@ -264,6 +265,17 @@ __global__ void __launch_bounds__(kIdxThreads)
         const int64_t after = static_cast<int64_t>(before) + add;
         if (after > static_cast<int64_t>(st.width) * st.page_size) no = 1;
         take = static_cast<int>((after + st.page_size - 1) / st.page_size) - pages_for(before, st.page_size);
+        if (add > 0 && before % st.page_size != 0) {
+          const int page = checked_page(st, st.table[seq * st.table_row + before / st.page_size]);
+          if (page >= 0 && st.refs[page] > 1) {
+            // Another sequence holds the page that the tokens would go to (a
+            // shrink has cut into a page that a fork shares): a copy of it is
+            // the first page taken.
+            ++take;
+            if (!copies) no = 1;
+            before = ~before;
+          }
+        }
       } else {
         no = 1;
       }
@@ -290,7 +302,11 @@ __global__ void __launch_bounds__(kIdxThreads)
     info[2] = refused;
     if (tokens != token) atomicExch(st.status, kDevBadIndex);
   }
-  __syncthreads();  // ws.at, before, token
+  if (threadIdx.x == 0) {
+    moves = 0;
+    if (!ok) ws.head->moves = 0;
+  }
+  __syncthreads();  // ws.at, before, token, moves
   if (positions != nullptr || slots != nullptr) {
     for (int t = threadIdx.x; t < tokens; t += kIdxThreads) {
       int64_t position = 0, slot = -1;
@@ -300,11 +316,12 @@ __global__ void __launch_bounds__(kIdxThreads)
           const int mid = (lo + hi) >> 1;
           if (ws.token[mid] <= t) lo = mid; else hi = mid;
         }
-        const int before = ws.before[lo];
+        const int own = ws.before[lo] < 0 ? 1 : 0;
+        const int before = own ? ~ws.before[lo] : ws.before[lo];
         const int pos = before + (t - ws.token[lo]);
         position = pos;
         if (ok) {
-          const int j = pos / st.page_size, held = pages_for(before, st.page_size);
+          const int j = pos / st.page_size, held = pages_for(before, st.page_size) - own;
           const int page = j < held ? checked_page(st, st.table[seqs[lo] * st.table_row + j])
                                     : page_of(ws.free_list, sh.free_at, st.seg, ws.at[lo] + j - held);
           if (page >= 0) slot = static_cast<int64_t>(page) * st.page_size + pos % st.page_size;
@@ -317,16 +334,26 @@ __global__ void __launch_bounds__(kIdxThreads)
   __syncthreads();  // the table has been read
   if (!ok) return;
   for (int i = warp; i < n; i += kIdxWarps) {
-    const int seq = seqs[i], before = ws.before[i];
+    const int own = ws.before[i] < 0 ? 1 : 0;
+    const int seq = seqs[i], before = own ? ~ws.before[i] : ws.before[i];
     const int after = before + max(counts[i], 0);
-    const int held = pages_for(before, st.page_size), wanted = pages_for(after, st.page_size);
+    const int held = pages_for(before, st.page_size) - own, wanted = pages_for(after, st.page_size);
     for (int j = held + lane; j < wanted; j += 32) {
       const int page = page_of(ws.free_list, sh.free_at, st.seg, ws.at[i] + j - held);
-      st.table[seq * st.table_row + j] = page;
+      int32_t* entry = st.table + seq * st.table_row + j;
+      if (own && j == held) {
+        const int to = atomicAdd(&moves, 1);  // (the order of the pairs makes no difference)
+        ws.src[to] = *entry;
+        ws.dst[to] = page;
+        atomicSub(st.refs + *entry, 1);
+      }
+      *entry = page;
       st.refs[page] = 1;
     }
     if (lane == 0) st.lens[seq] = after;
   }
+  __syncthreads();
+  if (threadIdx.x == 0) ws.head->moves = moves;
 }
 
 // One warp a sequence.
@@ -589,11 +616,19 @@ size_t cache_scratch_bytes(int64_t num_pages, int64_t n) {
 
 cudaError_t launch_cache_grow(const gemm_cache_t& c, int64_t n, const int32_t* seqs, const int32_t* counts,
                               int64_t tokens, int64_t* positions, int64_t* slots, int32_t* info, void* scratch,
-                              int* status, cudaStream_t stream) {
+                              int sms, int* status, cudaStream_t stream) {
   const PageState st = state_of(c, status);
-  return launch_pdl(cache_grow_kernel, dim3(idx_blocks(st)), dim3(kIdxThreads), 0, stream, st,
-                    scratch_at(scratch, c.num_pages, n), static_cast<int>(n), seqs, counts, static_cast<int>(tokens),
-                    positions, slots, info);
+  const Scratch ws = scratch_at(scratch, c.num_pages, n);
+  const cudaError_t e =
+      launch_pdl(cache_grow_kernel, dim3(idx_blocks(st)), dim3(kIdxThreads), 0, stream, st, ws, static_cast<int>(n),
+                 seqs, counts, static_cast<int>(tokens), positions, slots, info, c.pool_count > 0 ? 1 : 0);
+  if (e != cudaSuccess || c.pool_count == 0) return e;
+  // the pages that became a sequence's own, which the device alone knows: hardly ever one
+  CopyParams p = copy_params(c, status);
+  p.src = ws.src;
+  p.dst = ws.dst;
+  p.count = &ws.head->moves;
+  return launch_pdl(cache_copy_kernel, dim3(copy_grid(p, n, 1, sms)), dim3(kCopyThreads), 0, stream, p);
 }
 
 cudaError_t launch_cache_shrink(const gemm_cache_t& c, int64_t n, const int32_t* seqs, const int32_t* counts,

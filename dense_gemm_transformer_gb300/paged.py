@@ -140,16 +140,18 @@ class PagedOps:
             self._h and self._h.value, q, k_pages, v_pages, table, kv_lens, cu_q, max_q, max_kv, scale, softcap, window,
             out, return_lse, stream)
 
-    def cache_grow(self, table, lens, refs, page_size, seqs, counts, tokens, stream=None):
+    def cache_grow(self, table, lens, refs, page_size, seqs, counts, tokens, stream=None, pools=None):
         """Room for counts[i] more tokens of sequence seqs[i] (gemm_cache_grow):
         table int32 [sequences, width], lens int32 [sequences] and refs int32
         [pages] are updated in place; seqs (distinct) and counts are int32 on
-        the device, tokens the sum of counts.  Returns (positions, slots,
-        info): int64 [tokens] each, and int32 [3]: pages taken, pages missing,
-        sequences without room in their row; where one of the last two is not
-        0 nothing has been changed and every slot is -1."""
+        the device, tokens the sum of counts.  pools (as in cache_fork): where
+        the new tokens would go to a page that another sequence holds too, the
+        sequence gets a copy of it.  Returns (positions, slots, info): int64
+        [tokens] each, and int32 [3]: pages taken, pages missing, sequences
+        without room in their row or, without pools, on such a page; where one
+        of the last two is not 0 nothing has been changed and every slot is -1."""
         return (_native or _load(self._lib)).cache_grow(
-            self._h and self._h.value, table, lens, refs, page_size, seqs, counts, tokens, stream)
+            self._h and self._h.value, table, lens, refs, page_size, seqs, counts, tokens, stream, pools)
 
     def cache_shrink(self, table, lens, refs, page_size, seqs, counts=None, stream=None):
         """Takes the last counts[i] tokens of sequence seqs[i] back, all of them
@@ -200,8 +202,11 @@ class PagedCache:
         self.refs = torch.zeros(pages, dtype=torch.int32, device=device)
 
     def grow(self, seqs, counts, tokens):
-        """cache_grow: (positions, slots, info) of the new tokens."""
-        return cache_grow(self.table, self.lens, self.refs, self.page_size, seqs, counts, tokens)
+        """cache_grow over every layer: (positions, slots, info) of the new tokens."""
+        # (pages of another size than whole 16 bytes cannot be copied; fork refuses them, so none is ever shared)
+        copied = self.k[0, 0].numel() * self.k.element_size() % 16 == 0 if self.k.numel() else False
+        return cache_grow(self.table, self.lens, self.refs, self.page_size, seqs, counts, tokens,
+                          pools=(self.k, self.v) if copied else None)
 
     def shrink(self, seqs, counts=None):
         """cache_shrink: takes tokens back, all of them without counts."""
@@ -264,11 +269,11 @@ def paged_attention(q, k_pages, v_pages, table, kv_lens, cu_q=None, max_q=None, 
         return_lse, stream)
 
 
-def cache_grow(table, lens, refs, page_size, seqs, counts, tokens, stream=None):
+def cache_grow(table, lens, refs, page_size, seqs, counts, tokens, stream=None, pools=None):
     """PagedOps.cache_grow with the current device's default handle."""
     h = _handle()
     return (_native or _load(h._lib)).cache_grow(
-        h._h and h._h.value, table, lens, refs, page_size, seqs, counts, tokens, stream)
+        h._h and h._h.value, table, lens, refs, page_size, seqs, counts, tokens, stream, pools)
 
 
 def cache_shrink(table, lens, refs, page_size, seqs, counts=None, stream=None):

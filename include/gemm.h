@@ -549,10 +549,15 @@ typedef struct {
 
 /* Room for counts[i] more tokens of sequence seqs[i] (n of each; the
  * sequences distinct): info[0] pages taken, info[1] free pages missing,
- * info[2] sequences that their table row has no room for.  Where info[1] or
- * info[2] is not 0 nothing is changed and info[0] is 0.  For the new tokens
- * in order (`tokens` of them, the sum of counts): positions, and slots
- * (page * page_size + slot, -1 where nothing was taken), either or both NULL. */
+ * info[2] sequences that were refused.  Where info[1] or info[2] is not 0
+ * nothing is changed and info[0] is 0.  A sequence is refused when its table
+ * row has no room.  Where its new tokens would go to a page that another
+ * sequence holds too (one of them was shrunk into a page that a fork shares),
+ * it gets a copy of that page, in every pool, in its place: a page taken, the
+ * sequence's first.  With pool_count == 0 nothing can be copied, and it is
+ * refused.  For the new tokens in order (`tokens` of them, the sum of counts):
+ * positions, and slots (page * page_size + slot, -1 where nothing was taken),
+ * either or both NULL. */
 gemm_status_t gemm_cache_grow(gemm_handle_t h, const gemm_cache_t* c, int64_t n, const int32_t* seqs,
                               const int32_t* counts, int64_t tokens, int64_t* positions, int64_t* slots,
                               int32_t* info, void* stream);

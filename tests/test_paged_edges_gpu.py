@@ -1,0 +1,189 @@
+"""The operators on a paged cache where sequences share pages, where calls run
+on several streams, and at the ends of their arguments' ranges.  References are
+64-bit computations; the tolerances are those of test_paged_gpu.py, which
+derives them, unless a test says otherwise."""
+import math
+import random
+
+import pytest
+import torch
+
+import dense_gemm_transformer_gb300 as dg
+from tests.test_paged_gpu import BF16, FP16, FP32, Case, Model, _cache, _gen, _i32, _randn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def h():
+    dg.load(build_if_missing=True)
+    handle = dg.Gemm()
+    yield handle
+    handle.close()
+
+
+# ------------------------------------------------------- pages that are shared
+
+class OwnPages(Model):
+    """Model, with a sequence that appends to a page another one holds given its own copy of it (with pools), or
+    refused (without)."""
+
+    def shared(self, s, c):
+        return c > 0 and self.lens[s] % self.page != 0 and self.refs[self.rows[s][-1]] > 1
+
+    def grow(self, seqs, counts, pools=True):
+        own = [self.shared(s, c) for s, c in zip(seqs, counts)]
+        want = [self.need(self.lens[s] + c) - self.need(self.lens[s]) + o for s, c, o in zip(seqs, counts, own)]
+        missing = max(0, sum(want) - len(self.free()))
+        refused = sum(self.lens[s] + c > self.width * self.page or (o and not pools)
+                      for s, c, o in zip(seqs, counts, own))
+        positions = [self.lens[s] + i for s, c in zip(seqs, counts) for i in range(c)]
+        if missing or refused:
+            return positions, [-1] * len(positions), [0, missing, refused], []
+        slots, free, moves = [], self.free(), []
+        for s, c, w, o in zip(seqs, counts, want, own):
+            for i in range(w):
+                p = free.pop(0)
+                self.refs[p] = 1
+                if o and i == 0:
+                    moves.append((self.rows[s][-1], p))
+                    self.refs[self.rows[s][-1]] -= 1
+                    self.rows[s][-1] = p
+                else:
+                    self.rows[s].append(p)
+            for t in range(self.lens[s], self.lens[s] + c):
+                slots.append(self.rows[s][t // self.page] * self.page + t % self.page)
+            self.lens[s] += c
+        return positions, slots, [sum(want), 0, 0], moves
+
+
+@pytest.mark.parametrize("sequences,width,page,pages,seed", [(6, 5, 16, 14, 6), (40, 30, 16, 300, 1), (9, 7, 3, 24, 2),
+                                                              (30, 600, 32, 9000, 3), (1500, 4, 16, 5000, 4)])
+@pytest.mark.parametrize("pools", [True, False])
+def test_no_page_is_written_by_two_sequences(h, sequences, width, page, pages, seed, pools):
+    """Random growing, shrinking into shared pages, forking and compacting against plain Python, every sequence's
+    tokens written where grow says and read back through the table."""
+    rng = random.Random(seed)
+    m = OwnPages(sequences, width, page, pages)
+    table, lens, refs = _cache(sequences, width, pages)
+    pool = torch.full((pages, page, 1, 4), -1, dtype=torch.int32, device="cuda")
+    extra = torch.arange(2 * pages, dtype=torch.int32, device="cuda").view(2, pages, 1).repeat(1, 1, 4 * page)
+    mirror = extra.clone()
+    text = [[] for _ in range(sequences)]  # what each sequence's tokens should hold
+    stamp, copies = 0, 0
+
+    def follow(moves):
+        if moves:
+            src, dst = (torch.tensor(x, device="cuda") for x in zip(*moves))
+            mirror[:, dst] = mirror[:, src]
+
+    for step in range(60):
+        what = rng.choice(["grow", "grow", "shrink", "shrink", "fork", "fork", "compact"])
+        if what == "grow":
+            seqs = rng.sample(range(sequences), rng.randint(1, min(sequences, 300)))
+            counts = [rng.choice([0, 1, 1, page, rng.randint(0, page * min(width, 6) // 2)]) for _ in seqs]
+            if rng.random() < 0.5:  # few refusals for want of room
+                counts = [min(c, width * page - m.lens[s]) for s, c in zip(seqs, counts)]
+            positions, slots, info, moves = m.grow(seqs, counts, pools)
+            copies += len(moves)
+            got = h.cache_grow(table, lens, refs, page, _i32(seqs), _i32(counts), sum(counts),
+                               pools=(pool, extra) if pools else None)
+            assert got[0].tolist() == positions and got[1].tolist() == slots and got[2].tolist() == info
+            follow(moves)
+            if info[1:] == [0, 0] and slots:
+                values = list(range(stamp, stamp + len(slots)))
+                stamp += len(slots)
+                pool.flatten(0, 1)[got[1]] = _i32(values)[:, None, None]
+                for s, c in zip(seqs, counts):
+                    text[s] += values[:c]
+                    values = values[c:]
+        elif what == "shrink":
+            seqs = rng.sample(range(sequences), rng.randint(1, sequences // 2))
+            counts = None if rng.random() < 0.1 else [rng.randint(0, page + 3) for _ in seqs]
+            m.shrink(seqs, counts)
+            h.cache_shrink(table, lens, refs, page, _i32(seqs), None if counts is None else _i32(counts))
+            for s in seqs:
+                del text[s][m.lens[s]:]
+        elif what == "fork":
+            empty = [s for s in range(sequences) if m.lens[s] == 0]
+            held = [s for s in range(sequences) if m.lens[s] > 0]
+            children = empty[:rng.randint(0, len(empty))]
+            if not children or not held:
+                continue
+            parents = [rng.choice(held) for _ in children]
+            copied, info, moves = m.fork(parents, children)
+            got = h.cache_fork((pool, extra), table, lens, refs, page, _i32(parents), _i32(children))
+            assert got[0].tolist() == copied and got[1].tolist() == info
+            follow(moves)
+            if info[1:] == [0, 0]:
+                for p, c in zip(parents, children):
+                    text[c] = list(text[p])
+        else:
+            info, moves = m.compact()
+            assert h.cache_compact((pool, extra), table, refs).tolist() == info
+            follow(moves)
+        m.check(table, lens, refs)
+        assert torch.equal(extra, mirror)
+        rows, host = table.tolist(), pool[:, :, 0, 0].tolist()
+        for s in range(sequences):
+            assert text[s] == [host[rows[s][t // page]][t % page] for t in range(m.lens[s])], (step, s)
+    assert h.check_device() == 0
+    assert copies > 0 or not pools
+
+
+@pytest.mark.parametrize("who", ["child", "parent", "both"])
+def test_writing_after_a_shrink_leaves_the_other_sequence_as_it_was(who):
+    """Fork, give tokens back into a page that is shared, append others: attention of both against their own keys."""
+    heads, dim, page = 4, 64, 16
+    cache = dg.PagedCache(2, 12, page, heads, dim, 2, 4, BF16)
+    g = _gen(3)
+    keys = {0: [], 1: []}
+
+    def append(seqs, n):
+        x = _randn(g, (len(seqs) * n, 3 * heads, dim), FP32)
+        q, k, v = x.split(heads, 1)
+        positions, slots, info = cache.grow(_i32(seqs), _i32([n] * len(seqs)), len(seqs) * n)
+        assert info.tolist()[1:] == [0, 0] and int(slots.min()) >= 0
+        assert int(cache.refs[slots // page].max()) == 1  # nobody else's page
+        for layer in range(2):
+            q16 = cache.append(layer, q, k, v, positions, slots)
+        for i, s in enumerate(seqs):
+            at = slice(i * n, (i + 1) * n)
+            keys[s] += list(zip(k[at].to(BF16), v[at].to(BF16)))
+        return q16
+
+    append([0], 32)
+    cache.fork(_i32([0]), _i32([1]))
+    keys[1] = list(keys[0])
+    grown = [1] if who == "child" else [0] if who == "parent" else [0, 1]
+    cache.shrink(_i32(grown), _i32([3] * len(grown)))
+    for s in grown:
+        del keys[s][-3:]
+    append(grown, 3)
+    q = _randn(g, (2, heads, dim), BF16)
+    for layer in range(2):
+        out, lse = cache.attention(layer, q, return_lse=True)
+        c = Case.__new__(Case)
+        c.heads = c.kv_heads = heads
+        c.dim, c.q, c.lengths = dim, q, [(1, 32), (1, 32)]
+        c.keys, c.values = ([torch.stack([kv[i] for kv in keys[s]]) for s in (0, 1)] for i in (0, 1))
+        c.check(out, lse)
+    assert dg.default_handle().check_device() == 0
+
+
+def test_a_shared_page_without_pools_is_refused(h):
+    table, lens, refs = _cache(2, 4, 9)
+    h.cache_grow(table, lens, refs, 16, _i32([0]), _i32([32]), 32)
+    h.cache_fork((), table, lens, refs, 16, _i32([0]), _i32([1]))
+    h.cache_shrink(table, lens, refs, 16, _i32([1]), _i32([5]))
+    kept = table.clone(), lens.clone(), refs.clone()
+    positions, slots, info = h.cache_grow(table, lens, refs, 16, _i32([1]), _i32([5]), 5)
+    assert info.tolist() == [0, 0, 1] and slots.tolist() == [-1] * 5 and positions.tolist() == list(range(27, 32))
+    for a, b in zip(kept, (table, lens, refs)):
+        assert torch.equal(a, b)
+    # no tokens, and a page that is full, need no copy
+    assert h.cache_grow(table, lens, refs, 16, _i32([1, 0]), _i32([0, 2]), 2)[2].tolist() == [1, 0, 0]
+    # the other holder gives the page up: it is the sequence's own again
+    h.cache_shrink(table, lens, refs, 16, _i32([0]))
+    assert h.cache_grow(table, lens, refs, 16, _i32([1]), _i32([5]), 5)[2].tolist() == [0, 0, 0]
+    assert h.check_device() == 0
