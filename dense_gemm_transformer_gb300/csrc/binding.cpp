@@ -9,12 +9,14 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <optional>
 #include <string>
 
 #include "gemm.h"
@@ -77,8 +79,46 @@ gemm_handle_t handle_of(PyObject* o) {  // None: a closed handle, which the libr
   return static_cast<gemm_handle_t>(o == Py_None ? nullptr : address(o));
 }
 
-// The tensors of a call are on one device; its stream is the one given (a
-// torch stream or a raw handle) or the device's current one.
+// A stream as it is given: a torch stream or a raw handle.
+void* stream_of(PyObject* given) {
+  if (PyLong_Check(given)) return PyLong_AsLongLong(given) == 0 ? nullptr : address(given);
+  PyObject* raw = PyObject_GetAttrString(given, "cuda_stream");
+  if (raw == nullptr) throw Raised{};
+  void* s = PyLong_AsVoidPtr(raw);
+  Py_DECREF(raw);
+  if (PyErr_Occurred()) throw Raised{};
+  return s;
+}
+
+// While it lives, new tensors come from the memory of the call's stream, as
+// under torch.cuda.stream: a block of the current stream's could still be in
+// use by work that the call's stream does not wait for.
+class OutputsOn {
+ public:
+  OutputsOn(PyObject* given, const at::Tensor& like) {
+    if (given == Py_None || !like.is_cuda()) return;  // (another device's tensor is refused below)
+    const c10::DeviceIndex device = like.get_device();
+    void* raw = stream_of(given);
+    current_ = c10::cuda::getCurrentCUDAStream(device);
+    if (raw == current_->stream()) return;
+    guard_.emplace(raw == nullptr || raw == cudaStreamLegacy
+                       ? c10::cuda::getDefaultCUDAStream(device)
+                       : c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw), device));
+  }
+  // An output that the caller gets: it will most likely be read on the stream
+  // that is current for the caller.
+  at::Tensor give_back(at::Tensor t) const {
+    if (guard_) t.record_stream(*current_);
+    return t;
+  }
+
+ private:
+  std::optional<c10::cuda::CUDAStream> current_;
+  std::optional<c10::cuda::CUDAStreamGuard> guard_;
+};
+
+// The tensors of a call are on one device; its stream is the one given or the
+// device's current one.
 struct Device {
   int index = -1;
   void on(const at::Tensor& t, const char* name) {
@@ -88,13 +128,7 @@ struct Device {
   }
   void* stream(PyObject* given) const {
     if (given == Py_None) return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream();
-    if (PyLong_Check(given)) return address(given);
-    PyObject* raw = PyObject_GetAttrString(given, "cuda_stream");
-    if (raw == nullptr) throw Raised{};
-    void* s = PyLong_AsVoidPtr(raw);
-    Py_DECREF(raw);
-    if (PyErr_Occurred()) throw Raised{};
-    return s;
+    return stream_of(given);
   }
 };
 
@@ -142,10 +176,11 @@ const T* vector(Device& dev, const at::Tensor& t, const char* name, int64_t n, a
   return static_cast<const T*>(t.data_ptr());
 }
 
-// A new tensor on the device of `like`.
-at::Tensor fresh(const at::Tensor& like, const char* name, at::IntArrayRef sizes, at::ScalarType type) {
+// A new tensor on the device of `like`, for the caller.
+at::Tensor fresh(const OutputsOn& outputs, const at::Tensor& like, const char* name, at::IntArrayRef sizes,
+                 at::ScalarType type) {
   if (!like.is_cuda()) refuse(std::string(name) + " must be a CUDA tensor");
-  return at::empty(sizes, like.options().dtype(type));
+  return outputs.give_back(at::empty(sizes, like.options().dtype(type)));
 }
 
 PyObject* give(at::Tensor t) {
@@ -263,14 +298,15 @@ void run_rotary(PyObject* handle, const at::Tensor& q, PyObject* k_, PyObject* v
 // handle, q, k, positions, freqs, amplitude, interleaved, inverse, q_out, k_out, stream
 PyObject* rotary(PyObject* const* x) {
   const at::Tensor& q = tensor(x[1], "q");
-  const at::Tensor q_out = x[8] == Py_None ? fresh(q, "q", q.sizes(), q.scalar_type()) : tensor(x[8], "q_out");
+  const OutputsOn outputs(x[10], q);
+  const at::Tensor q_out = x[8] == Py_None ? fresh(outputs, q, "q", q.sizes(), q.scalar_type()) : tensor(x[8], "q_out");
   PyObject *qo = x[8] == Py_None ? give(q_out) : Py_NewRef(x[8]), *ko = nullptr;
   try {
     if (x[2] == Py_None) {
       ko = Py_NewRef(Py_None);
     } else if (x[9] == Py_None) {
       const at::Tensor& k = tensor(x[2], "k");
-      ko = give(fresh(k, "k", k.sizes(), k.scalar_type()));
+      ko = give(fresh(outputs, k, "k", k.sizes(), k.scalar_type()));
     } else {
       ko = Py_NewRef(x[9]);
     }
@@ -291,8 +327,9 @@ PyObject* rotary_append(PyObject* const* x) {
   const at::Tensor& q = tensor(x[1], "q");
   const at::Tensor& pool = tensor(x[6], "k_pages");
   if (x[2] == Py_None || x[3] == Py_None || x[5] == Py_None) refuse_type("k, v and slots are needed");
+  const OutputsOn outputs(x[12], q);
   const at::Tensor q_out =
-      x[11] == Py_None ? fresh(q, "q", q.sizes(), pool.scalar_type()) : tensor(x[11], "q_out");
+      x[11] == Py_None ? fresh(outputs, q, "q", q.sizes(), pool.scalar_type()) : tensor(x[11], "q_out");
   run_rotary(x[0], q, x[2], x[3], x[4], x[5], x[8], x[9], x[10], false, q_out, x[6], x[7], x[12]);
   return x[11] == Py_None ? give(q_out) : Py_NewRef(x[11]);
 }
@@ -345,9 +382,10 @@ PyObject* paged_attention(PyObject* const* x) {
   a.tokens = tokens;
   a.num_pages = k.size(0);
   a.max_kv = integer(x[8]);
+  const OutputsOn outputs(x[14], q);
   at::Tensor out;
   if (x[12] == Py_None) {
-    out = fresh(q, "q", q.sizes(), q.scalar_type());
+    out = fresh(outputs, q, "q", q.sizes(), q.scalar_type());
   } else {
     out = tensor(x[12], "out");
     if (out.sizes() != q.sizes() || out.scalar_type() != q.scalar_type()) refuse("out must have q's shape and type");
@@ -356,7 +394,7 @@ PyObject* paged_attention(PyObject* const* x) {
   at::Tensor lse;
   const bool with_lse = truth(x[13]);
   if (with_lse) {
-    lse = fresh(q, "q", {tokens, q.size(1)}, at::kFloat);
+    lse = fresh(outputs, q, "q", {tokens, q.size(1)}, at::kFloat);
     a.lse = static_cast<float*>(lse.data_ptr());
   }
   a.q = q.data_ptr();
@@ -485,8 +523,10 @@ PyObject* cache_grow(PyObject* const* x) {
   if (tokens < 0) refuse("tokens must not be negative");
   const int32_t* s = vector<int32_t>(dev, seqs, "seqs", n, at::kInt);
   const int32_t* k = vector<int32_t>(dev, tensor(x[6], "counts"), "counts", n, at::kInt);
-  at::Tensor positions = fresh(seqs, "seqs", {tokens}, at::kLong), slots = fresh(seqs, "seqs", {tokens}, at::kLong);
-  at::Tensor info = fresh(seqs, "seqs", {3}, at::kInt);
+  const OutputsOn outputs(x[8], seqs);
+  at::Tensor positions = fresh(outputs, seqs, "seqs", {tokens}, at::kLong);
+  at::Tensor slots = fresh(outputs, seqs, "seqs", {tokens}, at::kLong);
+  at::Tensor info = fresh(outputs, seqs, "seqs", {3}, at::kInt);
   call("gemm_cache_grow", g_lib.cache_grow, handle_of(x[0]), &c, n, s, k, tokens,
        static_cast<int64_t*>(positions.data_ptr()), static_cast<int64_t*>(slots.data_ptr()),
        static_cast<int32_t*>(info.data_ptr()), dev.stream(x[8]));
@@ -513,7 +553,9 @@ PyObject* cache_fork(PyObject* const* x) {
   const int64_t n = parents.numel();
   const int32_t* p = vector<int32_t>(dev, parents, "parents", n, at::kInt);
   const int32_t* k = vector<int32_t>(dev, tensor(x[7], "children"), "children", n, at::kInt);
-  at::Tensor copied = fresh(parents, "parents", {n}, at::kInt), info = fresh(parents, "parents", {3}, at::kInt);
+  const OutputsOn outputs(x[8], parents);
+  at::Tensor copied = fresh(outputs, parents, "parents", {n}, at::kInt);
+  at::Tensor info = fresh(outputs, parents, "parents", {3}, at::kInt);
   call("gemm_cache_fork", g_lib.cache_fork, handle_of(x[0]), &c, n, p, k, static_cast<int32_t*>(copied.data_ptr()),
        static_cast<int32_t*>(info.data_ptr()), dev.stream(x[8]));
   return pack({copied, info});
@@ -524,7 +566,8 @@ PyObject* cache_compact(PyObject* const* x) {
   Device dev;
   const gemm_cache_t c = cache_of(dev, x[1], x[2], nullptr, x[3], nullptr);
   const at::Tensor& table = tensor(x[2], "table");
-  at::Tensor info = fresh(table, "table", {2}, at::kInt);
+  const OutputsOn outputs(x[4], table);
+  at::Tensor info = fresh(outputs, table, "table", {2}, at::kInt);
   call("gemm_cache_compact", g_lib.cache_compact, handle_of(x[0]), &c, static_cast<int32_t*>(info.data_ptr()),
        dev.stream(x[4]));
   return give(std::move(info));

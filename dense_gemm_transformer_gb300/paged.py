@@ -3,7 +3,9 @@
 Argument marshalling only, like the rest of the binding, here by a native
 module (csrc/binding.cpp): it checks the tensors and calls the C ABI
 (include/gemm.h, "Generation on a paged cache"), which also holds the
-operators' exact meaning.  One step of generation:
+operators' exact meaning.  Calls run on the current stream or on `stream` (a
+torch stream or a raw handle), whose memory new outputs then come from.  One
+step of generation:
 
     freqs, amplitude = dg.rotary_frequencies(128, base=10000.0, device="cuda")   # once
     positions, slots, info = dg.cache_grow(table, lens, refs, page_size, seqs, counts, tokens)
@@ -226,10 +228,24 @@ class PagedCache:
 
     def attention(self, layer, q, seqs=None, **kwargs):
         """paged_attention over one layer's pools, of the sequences seqs (an
-        index tensor; None: all, in order)."""
+        index tensor; None: all, in order).  With a stream (a torch stream or
+        a raw handle), all of it runs there."""
+        stream = kwargs.pop("stream", None)
+        if stream is not None:
+            import torch
+            with torch.cuda.stream(_torch_stream(stream)):
+                return self.attention(layer, q, seqs, **kwargs)
         table = self.table if seqs is None else self.table.index_select(0, seqs)
         lens = self.lens if seqs is None else self.lens.index_select(0, seqs)
         return paged_attention(q, self.k[layer], self.v[layer], table, lens, **kwargs)
+
+
+def _torch_stream(stream):
+    """A torch stream for a stream as the calls take it."""
+    import torch
+    if not isinstance(stream, int):
+        return stream
+    return torch.cuda.default_stream() if stream in (0, 1) else torch.cuda.ExternalStream(stream)
 
 
 def _handle():

@@ -187,3 +187,65 @@ def test_a_shared_page_without_pools_is_refused(h):
     h.cache_shrink(table, lens, refs, 16, _i32([0]))
     assert h.cache_grow(table, lens, refs, 16, _i32([1]), _i32([5]), 5)[2].tolist() == [0, 0, 0]
     assert h.check_device() == 0
+
+
+# -------------------------------------------------------- streams and handles
+
+def test_cache_attention_gathers_on_the_stream_it_runs_on():
+    """seqs and stream together: nothing of the call waits for the current stream, or runs on it."""
+    cache = dg.PagedCache(1, 40, 16, 2, 64, 4, 16, BF16)
+    seqs = torch.tensor([3, 1], device="cuda")
+    positions, slots, info = cache.grow(_i32([0, 1, 2, 3]), _i32([50, 60, 70, 80]), 260)
+    x = _randn(_gen(1), (260, 8, 64), FP32)
+    cache.append(0, x[:, :4], x[:, 4:6], x[:, 6:], positions, slots)
+    q = _randn(_gen(2), (2, 4, 64), BF16)
+    want = cache.attention(0, q, seqs)
+    side, raw = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    host = torch.empty(want.shape, dtype=BF16, pin_memory=True)
+    for stream, given in ((side, side), (raw, raw.cuda_stream)):
+        cache.attention(0, q, seqs, stream=given)  # (its memory is allocated)
+        torch.cuda.synchronize()
+        host.zero_()
+        busy = torch.cuda.Event()
+        torch.cuda._sleep(10 ** 9)
+        busy.record()
+        got = cache.attention(0, q, seqs, stream=given)
+        stream.synchronize()
+        assert not busy.query()  # the current stream has not come that far
+        with torch.cuda.stream(stream):
+            host.copy_(got, non_blocking=True)
+        stream.synchronize()
+        assert not busy.query()
+        torch.cuda.synchronize()
+        assert torch.equal(host, want.cpu())
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_outputs_belong_to_the_stream_of_the_call(h, raw):
+    """A new output comes from the memory of the call's stream: never a block that work of the current stream, not
+    yet run, still uses."""
+    c = Case([(1, 40)] * 64, 4, 2, 64, 16, BF16, seed=1)
+    freqs, _ = dg.rotary_frequencies(64, device="cuda")
+    positions = torch.arange(64, device="cuda")
+    table, lens, refs = _cache(3, 9, 30)
+    seqs, counts = _i32([0, 2]), _i32([20, 33])
+    side = torch.cuda.Stream()
+    given = side.cuda_stream if raw else side
+    torch.cuda.synchronize()
+
+    def stream_of(t):
+        at = t.data_ptr()
+        return next(s["stream"] for s in torch.cuda.memory_snapshot()
+                    if s["address"] <= at < s["address"] + s["total_size"])
+
+    for call in (lambda s: h.paged_attention(c.q, c.k, c.v, c.table, c.lens, return_lse=True, stream=s),
+                 lambda s: h.rotary(c.q, c.q, positions, freqs, stream=s),
+                 lambda s: (h.rotary_append(c.q[:1], c.q[:1, :2], c.q[:1, :2], None, positions[:1], c.k, c.v, stream=s),),
+                 lambda s: h.cache_grow(table, lens, refs, 16, seqs, counts, 53, stream=s)):
+        for t in call(given):
+            assert stream_of(t) == side.cuda_stream
+        for t in call(None):
+            assert stream_of(t) == torch.cuda.current_stream().cuda_stream
+        torch.cuda.synchronize()
+    assert h.check_device() == 0
