@@ -906,10 +906,15 @@ gemm_status_t gemm_destroy(gemm_handle_t h) {
   gemm_status_t st = cuda_status(cudaDeviceSynchronize());
   if (h->ws) cudaFree(h->ws);
   if (h->ws_t) cudaFree(h->ws_t);
-  for (void* block : h->attn_ws)
-    if (block) cudaFree(block);
-  for (void* block : h->cache_ws)
-    if (block) cudaFree(block);
+  while (h->paged_scratch != nullptr) {
+    dgt::StreamScratch* s = h->paged_scratch;
+    h->paged_scratch = s->next;
+    for (void* block : s->attn)
+      if (block) cudaFree(block);
+    for (void* block : s->cache)
+      if (block) cudaFree(block);
+    delete s;
+  }
   if (h->d_status) cudaFree(h->d_status);
   delete h->tma_cache;
   cudaSetDevice(prev);

@@ -4,6 +4,8 @@
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
+#include <new>
 
 #include "gemm.h"
 #include "handle.h"
@@ -109,31 +111,64 @@ gemm_status_t check_state(const gemm_cache_t& c, bool lens) {
   return GEMM_OK;
 }
 
-// A device block of `bytes`, zeroed when it is new.
-gemm_status_t device_block(void** block, size_t bytes) {
-  if (*block != nullptr) return GEMM_OK;
+// A new device block of `bytes` zeros.
+gemm_status_t zeroed_block(void** block, size_t bytes) {
+  // a stream of its own for the zeros: the caller's may not wait for the
+  // default one, or may be recording a graph, which the zeros are no part of
+  cudaStream_t stream;
   void* p = nullptr;
   if (cudaMalloc(&p, bytes) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_ALLOC;
   }
-  // the caller's stream may not wait for the default one
-  if (cudaMemset(p, 0, bytes) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess) {
-    cudaGetLastError();
+  cudaError_t e = cudaStreamCreateWithFlags(&stream, cudaStreamNonBlocking);
+  if (e == cudaSuccess) {
+    e = cudaMemsetAsync(p, 0, bytes, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    cudaStreamDestroy(stream);
+  }
+  if (e != cudaSuccess) {
     cudaFree(p);
-    return GEMM_ERR_CUDA;
+    return cuda_status(e);
   }
   *block = p;
   return GEMM_OK;
 }
 
-// The smallest block of the handle's that holds `bytes`: block i has 2^i MiB.
-gemm_status_t scratch_of(void* (&blocks)[dgt::kScratchBlocks], size_t bytes, void** out) {
+// The smallest block that holds `bytes` of the handle's scratch for `stream`
+// (block i has 2^i MiB); `blocks`: which of it.
+gemm_status_t scratch_of(gemm_handle_t h, void* (dgt::StreamScratch::*blocks)[dgt::kScratchBlocks], void* stream,
+                         size_t bytes, void** out) {
   int i = 0;
   while ((size_t(1) << (20 + i)) < bytes) ++i;
   if (i >= dgt::kScratchBlocks) return GEMM_ERR_ALLOC;
-  const gemm_status_t st = device_block(&blocks[i], size_t(1) << (20 + i));
-  *out = blocks[i];
+  unsigned long long id = reinterpret_cast<uintptr_t>(stream);
+  cudaStreamCaptureStatus state;
+  cudaError_t e = cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &state);
+  const bool captured = e == cudaSuccess && state != cudaStreamCaptureStatusNone;
+  if (e == cudaSuccess && !captured) e = cudaStreamGetId(static_cast<cudaStream_t>(stream), &id);
+  if (e != cudaSuccess) return cuda_status(e);
+  std::lock_guard<std::mutex> lock(h->paged_lock);
+  dgt::StreamScratch* s = h->paged_scratch;
+  while (s != nullptr && (s->stream != id || s->captured != captured)) s = s->next;
+  if (s == nullptr) {
+    s = new (std::nothrow) dgt::StreamScratch{};
+    if (s == nullptr) return GEMM_ERR_ALLOC;
+    s->stream = id;
+    s->captured = captured;
+    s->next = h->paged_scratch;
+    h->paged_scratch = s;
+  }
+  void** block = &(s->*blocks)[i];
+  gemm_status_t st = GEMM_OK;
+  if (*block == nullptr) {
+    // (while a stream is being captured, only a thread in this mode may allocate)
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    st = zeroed_block(block, size_t(1) << (20 + i));
+    cudaThreadExchangeStreamCaptureMode(&mode);
+  }
+  *out = *block;
   return st;
 }
 
@@ -157,7 +192,7 @@ gemm_status_t gemm_paged_attention(gemm_handle_t h, const gemm_paged_attention_t
   const dgt::PagedPlan plan = dgt::paged_attention_plan(*a, h->sms);
   if (plan.tile_parts > kMaxTileParts) return GEMM_ERR_INVALID_VALUE;
   void* ws;
-  st = scratch_of(h->attn_ws, dgt::paged_scratch_bytes(plan, a->head_dim), &ws);
+  st = scratch_of(h, &dgt::StreamScratch::attn, stream, dgt::paged_scratch_bytes(plan, a->head_dim), &ws);
   if (st != GEMM_OK) return st;
   dgt::last_main_launch().valid = false;
   st = cuda_status(dgt::launch_paged_attention(*a, plan, ws, h->sms, static_cast<uint64_t>(h->opt_wait_us) * 1000u,
@@ -172,6 +207,7 @@ gemm_status_t gemm_paged_attention(gemm_handle_t h, const gemm_paged_attention_t
   p.stages = plan.stages;
   p.grid = plan.grid;
   p.kernels = plan.kernels;
+  std::lock_guard<std::mutex> lock(h->paged_lock);
   h->plan = p;
   h->null_shape = dgt::last_main_launch();
   return GEMM_OK;
@@ -188,7 +224,7 @@ gemm_status_t gemm_cache_grow(gemm_handle_t h, const gemm_cache_t* c, int64_t n,
   if (!aligned(seqs, 4) || !aligned(counts, 4) || !aligned(info, 4) || !aligned(positions, 8) || !aligned(slots, 8))
     return GEMM_ERR_MISALIGNED;
   void* ws;
-  st = scratch_of(h->cache_ws, dgt::cache_scratch_bytes(c->num_pages, n), &ws);
+  st = scratch_of(h, &dgt::StreamScratch::cache, stream, dgt::cache_scratch_bytes(c->num_pages, n), &ws);
   if (st != GEMM_OK) return st;
   return cuda_status(dgt::launch_cache_grow(*c, n, seqs, counts, tokens, positions, slots, info, ws, h->sms,
                                             h->d_status, static_cast<cudaStream_t>(stream)));
@@ -215,7 +251,7 @@ gemm_status_t gemm_cache_fork(gemm_handle_t h, const gemm_cache_t* c, int64_t n,
   if (!aligned(parents, 4) || !aligned(children, 4) || !aligned(copied, 4) || !aligned(info, 4))
     return GEMM_ERR_MISALIGNED;
   void* ws;
-  st = scratch_of(h->cache_ws, dgt::cache_scratch_bytes(c->num_pages, n), &ws);
+  st = scratch_of(h, &dgt::StreamScratch::cache, stream, dgt::cache_scratch_bytes(c->num_pages, n), &ws);
   if (st != GEMM_OK) return st;
   return cuda_status(dgt::launch_cache_fork(*c, n, parents, children, copied, info, ws, h->sms, h->d_status,
                                             static_cast<cudaStream_t>(stream)));
@@ -228,7 +264,7 @@ gemm_status_t gemm_cache_compact(gemm_handle_t h, const gemm_cache_t* c, int32_t
   if (info == nullptr) return GEMM_ERR_INVALID_VALUE;
   if (!aligned(info, 4)) return GEMM_ERR_MISALIGNED;
   void* ws;
-  st = scratch_of(h->cache_ws, dgt::cache_scratch_bytes(c->num_pages, 0), &ws);
+  st = scratch_of(h, &dgt::StreamScratch::cache, stream, dgt::cache_scratch_bytes(c->num_pages, 0), &ws);
   if (st != GEMM_OK) return st;
   return cuda_status(
       dgt::launch_cache_compact(*c, info, ws, h->sms, h->d_status, static_cast<cudaStream_t>(stream)));

@@ -48,7 +48,8 @@
  * between calls) and a scratch workspace (split-K partial sums, re-packed
  * and transposed operands) that grows on demand and is freed by
  * gemm_destroy.  A handle is bound to the device that was current at
- * gemm_create and must not be used from two streams at the same time.
+ * gemm_create and must not be used from two streams at the same time, except
+ * for generation on a paged cache (below).
  *
  * Errors: every call returns a status and never throws.  Arguments are checked
  * before anything is launched; a failed check launches nothing and leaves C
@@ -420,6 +421,13 @@ gemm_status_t gemm_attention_forward(gemm_handle_t h, int64_t problems, int64_t 
  * pages of its row of the page table, token t in slot t % page_size of page
  * table[seq][t / page_size].
  *
+ * These calls may be made on several streams and from several threads with
+ * one handle: it keeps scratch for each stream that they have run on, until
+ * gemm_destroy (gemm_get_plan then reports the last one that was launched).
+ * Calls that graphs capture on one stream share one such scratch, so those
+ * graphs must not run at the same time.  The first call of a size on a stream,
+ * and the first that is captured there, allocates, in a capture too.
+ *
  * Whole numbers that live in device memory (pages, slots, lengths, offsets)
  * are checked by the kernels: one outside its range is left out (what
  * depends on it is undefined or not written, nothing else is), and
@@ -523,7 +531,8 @@ typedef struct {
  * a negative window; GEMM_ERR_NOT_SUPPORTED for a head_dim other than 64 and
  * 128 or a page_size that is not a multiple of 16; GEMM_ERR_MISALIGNED for
  * q, pages or out not 16-byte aligned or a stride of theirs that is not a
- * multiple of 8 elements.  tokens == 0 or sequences == 0 is a no-op.
+ * multiple of 8 elements; GEMM_ERR_ALLOC when scratch could not be allocated.
+ * tokens == 0 or sequences == 0 is a no-op.
  * gemm_get_plan reports GEMM_FAMILY_PAGED_ATTENTION, the rows and keys of a
  * tile, and in split_k the most parts a sequence's keys are split into. */
 gemm_status_t gemm_paged_attention(gemm_handle_t h, const gemm_paged_attention_t* a, void* stream);
@@ -589,8 +598,7 @@ gemm_status_t gemm_cache_copy(gemm_handle_t h, const gemm_cache_t* c, int64_t n,
  * or needed pointer, negative sizes, more than 8 pools, or more than 2^30
  * pages; GEMM_ERR_MISALIGNED for pools not 16-byte aligned, with strides that
  * are not, or page_bytes not a multiple of 16; GEMM_ERR_ALLOC when scratch
- * could not be allocated (the first call for a larger cache allocates; make
- * it before any stream capture). */
+ * could not be allocated. */
 
 /* A static string naming a status code. */
 const char* gemm_status_string(gemm_status_t s);

@@ -249,3 +249,77 @@ def test_outputs_belong_to_the_stream_of_the_call(h, raw):
             assert stream_of(t) == torch.cuda.current_stream().cuda_stream
         torch.cuda.synchronize()
     assert h.check_device() == 0
+
+
+def test_one_handle_on_several_streams(h):
+    """Calls whose parts and counters live in the handle, at the same time on four streams: each as it is alone."""
+    cases = [Case([(1, 9000 + 500 * i), (1, 300)], 12, 2, 128, 16, BF16, seed=i) for i in range(2)]
+    cases += [Case([(150, 2500 + 300 * i), (2, 900)], 8, 2, 64, 16, FP16, seed=5 + i) for i in range(2)]
+    want = [tuple(t.clone() for t in c.run(h)) for c in cases]
+    assert h.plan()["split_k"] > 1
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[] for _ in cases]
+    for _ in range(40):
+        for c, s, g in zip(cases, streams, got):
+            g.append(c.run(h, stream=s))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for out, lse in g:
+            assert torch.equal(out, w[0]) and torch.equal(lse, w[1])
+    # and afterwards
+    for c, w in zip(cases, want):
+        assert torch.equal(c.run(h)[0], w[0])
+    assert h.check_device() == 0
+
+
+def test_page_management_on_several_streams(h):
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    states = []
+    for i in range(3):
+        table, lens, refs = _cache(40, 50, 60000 + 5000 * i)
+        states.append((table, lens, refs, Model(40, 50, 16, 60000 + 5000 * i)))
+    torch.cuda.synchronize()
+    for step in range(20):
+        got = []
+        for i, ((table, lens, refs, m), s) in enumerate(zip(states, streams)):
+            seqs, counts = list(range(step % 7, 40, 2 + i)), []
+            counts = [1 + (step * 7 + x) % 30 for x in seqs]
+            a, b = _i32(seqs), _i32(counts)
+            torch.cuda.current_stream().synchronize()
+            got.append((h.cache_grow(table, lens, refs, 16, a, b, sum(counts), stream=s), seqs, counts, a, b))
+        torch.cuda.synchronize()
+        for (table, lens, refs, m), ((positions, slots, info), seqs, counts, _, _) in zip(states, got):
+            want = m.grow(seqs, counts)
+            assert positions.tolist() == want[0] and slots.tolist() == want[1] and info.tolist() == want[2]
+    for table, lens, refs, m in states:
+        m.check(table, lens, refs)
+    assert h.check_device() == 0
+
+
+@pytest.mark.parametrize("lengths", [[(1, 3000)] * 3, [(130, 4000), (1, 50)]])
+def test_a_first_call_can_be_captured(lengths):
+    """A handle that has no scratch yet, in a graph."""
+    handle = dg.Gemm()
+    c = Case(lengths, 8, 2, 64, 16, BF16, seed=6)
+    out = torch.zeros_like(c.q)
+    table, lens, refs = _cache(3, 9, 30)
+    seqs, counts = _i32([0, 2]), _i32([20, 33])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        handle.paged_attention(c.q, c.k, c.v, c.table, c.lens, cu_q=c.cu, max_q=c.max_q, out=out)
+        grown = handle.cache_grow(table, lens, refs, 16, seqs, counts, 53)
+    for _ in range(3):
+        lens.zero_(), refs.zero_(), table.fill_(-1), out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = c.run(handle)[0]
+        assert torch.equal(out, want)
+        m = Model(3, 9, 16, 30)
+        assert [t.tolist() for t in grown] == list(m.grow([0, 2], [20, 33]))
+        m.check(table, lens, refs)
+    assert handle.check_device() == 0
+    del graph
+    torch.cuda.synchronize()
+    handle.close()
