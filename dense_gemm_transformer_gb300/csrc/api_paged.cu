@@ -26,6 +26,15 @@ gemm_status_t cuda_status(cudaError_t e) {
   return GEMM_ERR_CUDA;
 }
 
+// The handle's device must be the current one: launches, attributes and
+// allocations go to that.
+gemm_status_t check_device(gemm_handle_t h) {
+  int device;
+  const cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return cuda_status(e);
+  return device == h->device ? GEMM_OK : GEMM_ERR_INVALID_VALUE;
+}
+
 gemm_status_t check_rotary(const gemm_rotary_t& a) {
   if (!known_type(a.in_type) || !known_type(a.out_type)) return GEMM_ERR_INVALID_VALUE;
   if ((a.interleaved | a.inverse) & ~1) return GEMM_ERR_INVALID_VALUE;
@@ -178,9 +187,11 @@ extern "C" {
 
 gemm_status_t gemm_rotary(gemm_handle_t h, const gemm_rotary_t* a, void* stream) {
   if (h == nullptr || a == nullptr) return GEMM_ERR_INVALID_VALUE;
-  const gemm_status_t st = check_rotary(*a);
+  gemm_status_t st = check_rotary(*a);
   if (st != GEMM_OK) return st;
   if (a->tokens == 0 || (a->heads == 0 && (a->k == nullptr || a->kv_heads == 0))) return GEMM_OK;
+  st = check_device(h);
+  if (st != GEMM_OK) return st;
   return cuda_status(dgt::launch_rotary(*a, h->sms, h->d_status, static_cast<cudaStream_t>(stream)));
 }
 
@@ -189,6 +200,8 @@ gemm_status_t gemm_paged_attention(gemm_handle_t h, const gemm_paged_attention_t
   gemm_status_t st = check_attention(*a);
   if (st != GEMM_OK) return st;
   if (a->tokens == 0 || a->sequences == 0) return GEMM_OK;
+  st = check_device(h);
+  if (st != GEMM_OK) return st;
   const dgt::PagedPlan plan = dgt::paged_attention_plan(*a, h->sms);
   if (plan.tile_parts > kMaxTileParts) return GEMM_ERR_INVALID_VALUE;
   void* ws;
@@ -223,6 +236,8 @@ gemm_status_t gemm_cache_grow(gemm_handle_t h, const gemm_cache_t* c, int64_t n,
     return GEMM_ERR_INVALID_VALUE;
   if (!aligned(seqs, 4) || !aligned(counts, 4) || !aligned(info, 4) || !aligned(positions, 8) || !aligned(slots, 8))
     return GEMM_ERR_MISALIGNED;
+  st = check_device(h);
+  if (st != GEMM_OK) return st;
   void* ws;
   st = scratch_of(h, &dgt::StreamScratch::cache, stream, dgt::cache_scratch_bytes(c->num_pages, n), &ws);
   if (st != GEMM_OK) return st;
@@ -238,6 +253,8 @@ gemm_status_t gemm_cache_shrink(gemm_handle_t h, const gemm_cache_t* c, int64_t 
   if (n == 0) return GEMM_OK;
   if (seqs == nullptr) return GEMM_ERR_INVALID_VALUE;
   if (!aligned(seqs, 4) || !aligned(counts, 4)) return GEMM_ERR_MISALIGNED;
+  st = check_device(h);
+  if (st != GEMM_OK) return st;
   return cuda_status(dgt::launch_cache_shrink(*c, n, seqs, counts, h->d_status, static_cast<cudaStream_t>(stream)));
 }
 
@@ -250,6 +267,8 @@ gemm_status_t gemm_cache_fork(gemm_handle_t h, const gemm_cache_t* c, int64_t n,
     return GEMM_ERR_INVALID_VALUE;
   if (!aligned(parents, 4) || !aligned(children, 4) || !aligned(copied, 4) || !aligned(info, 4))
     return GEMM_ERR_MISALIGNED;
+  st = check_device(h);
+  if (st != GEMM_OK) return st;
   void* ws;
   st = scratch_of(h, &dgt::StreamScratch::cache, stream, dgt::cache_scratch_bytes(c->num_pages, n), &ws);
   if (st != GEMM_OK) return st;
@@ -263,6 +282,8 @@ gemm_status_t gemm_cache_compact(gemm_handle_t h, const gemm_cache_t* c, int32_t
   if (st != GEMM_OK) return st;
   if (info == nullptr) return GEMM_ERR_INVALID_VALUE;
   if (!aligned(info, 4)) return GEMM_ERR_MISALIGNED;
+  st = check_device(h);
+  if (st != GEMM_OK) return st;
   void* ws;
   st = scratch_of(h, &dgt::StreamScratch::cache, stream, dgt::cache_scratch_bytes(c->num_pages, 0), &ws);
   if (st != GEMM_OK) return st;
@@ -272,11 +293,13 @@ gemm_status_t gemm_cache_compact(gemm_handle_t h, const gemm_cache_t* c, int32_t
 
 gemm_status_t gemm_cache_copy(gemm_handle_t h, const gemm_cache_t* c, int64_t n, const int32_t* src,
                               const int32_t* dst, void* stream) {
-  const gemm_status_t st = check_cache(h, c, n, true);
+  gemm_status_t st = check_cache(h, c, n, true);
   if (st != GEMM_OK) return st;
   if (n == 0) return GEMM_OK;
   if (src == nullptr || dst == nullptr) return GEMM_ERR_INVALID_VALUE;
   if (!aligned(src, 4) || !aligned(dst, 4)) return GEMM_ERR_MISALIGNED;
+  st = check_device(h);
+  if (st != GEMM_OK) return st;
   return cuda_status(
       dgt::launch_cache_copy(*c, n, src, dst, h->sms, h->d_status, static_cast<cudaStream_t>(stream)));
 }

@@ -117,13 +117,18 @@ class OutputsOn {
   std::optional<c10::cuda::CUDAStreamGuard> guard_;
 };
 
-// The tensors of a call are on one device; its stream is the one given or the
-// device's current one.
+// The tensors of a call are on the current device (as the library asks of its
+// handle); its stream is the one given or the device's current one.
 struct Device {
   int index = -1;
   void on(const at::Tensor& t, const char* name) {
     if (!t.is_cuda()) refuse(std::string(name) + " must be a CUDA tensor");
-    if (index < 0) index = t.get_device();
+    if (index < 0) {
+      c10::DeviceIndex current = -1;
+      if (c10::cuda::GetDevice(&current) != cudaSuccess) current = -1;
+      index = t.get_device();
+      if (index != current) refuse(std::string(name) + " must be on the current device");
+    }
     if (t.get_device() != index) refuse("all tensors must be on one device");
   }
   void* stream(PyObject* given) const {

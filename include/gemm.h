@@ -421,6 +421,7 @@ gemm_status_t gemm_attention_forward(gemm_handle_t h, int64_t problems, int64_t 
  * pages of its row of the page table, token t in slot t % page_size of page
  * table[seq][t / page_size].
  *
+ * The handle's device must be the current one (else GEMM_ERR_INVALID_VALUE).
  * These calls may be made on several streams and from several threads with
  * one handle: it keeps scratch for each stream that they have run on, until
  * gemm_destroy (gemm_get_plan then reports the last one that was launched).

@@ -323,3 +323,21 @@ def test_a_first_call_can_be_captured(lengths):
     del graph
     torch.cuda.synchronize()
     handle.close()
+
+
+def test_a_handle_of_another_device_is_refused(h):
+    """The check comes before anything else of a handle is read: a handle that is its first word, the device, and
+    zeros, is refused by every call."""
+    import ctypes
+    from tests import test_paged_host as host
+    lib = dg.load()
+    fake = (ctypes.c_int32 * 4096)(torch.cuda.current_device() + 1)
+    handle = ctypes.cast(fake, ctypes.c_void_p)
+    assert lib.gemm_rotary(handle, host._pack("gemm_rotary_t", host.ROTARY), None) == host.INVALID
+    assert lib.gemm_paged_attention(handle, host._pack("gemm_paged_attention_t", host.ATTENTION), None) == host.INVALID
+    c, p = host._cache(), host.P
+    assert lib.gemm_cache_grow(handle, c, 1, p, p, 1, p, p, p, None) == host.INVALID
+    assert lib.gemm_cache_shrink(handle, c, 1, p, p, None) == host.INVALID
+    assert lib.gemm_cache_fork(handle, c, 1, p, p, p, p, None) == host.INVALID
+    assert lib.gemm_cache_compact(handle, c, p, None) == host.INVALID
+    assert lib.gemm_cache_copy(handle, c, 1, p, p, None) == host.INVALID

@@ -1,7 +1,9 @@
 """Refusals and no-ops at the ends of the paged operators' arguments, without a GPU (as in test_paged_host.py)."""
 import pytest
+import torch
 
 import dense_gemm_transformer_gb300 as dg
+from dense_gemm_transformer_gb300 import paged
 from tests.test_paged_host import H, INVALID, MISALIGNED, P, _cache
 
 
@@ -17,3 +19,43 @@ def test_grow_checks_its_pools(lib):
                                  ({}, (P + 8, 2, 1 << 20, 8192), MISALIGNED), ({}, (P, 2, 1 << 20, 8), MISALIGNED),
                                  ({}, (0, 2, 1 << 20, 8192), INVALID)]:
         assert lib.gemm_cache_grow(H, _cache(pool, **change), 1, P, P, 1, P, P, P, None) == status
+
+
+def _tensor_of(device, shape, dtype):
+    """A tensor said to be on a CUDA device, over an address that nothing reads."""
+    count = 1
+    stride = []
+    for n in reversed(shape):
+        stride.insert(0, count)
+        count *= n
+    storage = torch._C._construct_storage_from_data_pointer(P, torch.device(device), count * dtype.itemsize)
+    meta = {"dtype": dtype, "storage_offset": 0, "size": torch.Size(shape), "stride": tuple(stride),
+            "device": torch.device(device), "storage": storage}
+    return torch._C._construct_CUDA_Tensor_From_Storage_And_Metadata(meta, storage)
+
+
+def test_tensors_of_another_device_are_refused(lib):
+    """Before the library is called: its handle there is None."""
+    ops = paged.PagedOps()
+    ops._lib, ops._h = lib, None
+    device = "cuda:7"
+    x = _tensor_of(device, (4, 2, 64), torch.bfloat16)
+    pages = _tensor_of(device, (3, 16, 2, 64), torch.bfloat16)
+    table, lens = _tensor_of(device, (4, 3), torch.int32), _tensor_of(device, (4,), torch.int32)
+    refs, slots = _tensor_of(device, (3,), torch.int32), _tensor_of(device, (4,), torch.int64)
+    with pytest.raises(ValueError, match="current device"):
+        ops.rotary(x, None, slots, slots, q_out=x)
+    with pytest.raises(ValueError, match="current device"):
+        ops.rotary_append(x, x, x, None, slots, pages, pages, q_out=x)
+    with pytest.raises(ValueError, match="current device"):
+        ops.paged_attention(x, pages, pages, table, lens, out=x)
+    with pytest.raises(ValueError, match="current device"):
+        ops.cache_grow(table, lens, refs, 16, lens, lens, 4)
+    with pytest.raises(ValueError, match="current device"):
+        ops.cache_shrink(table, lens, refs, 16, lens)
+    with pytest.raises(ValueError, match="current device"):
+        ops.cache_fork((pages,), table, lens, refs, 16, lens, lens)
+    with pytest.raises(ValueError, match="current device"):
+        ops.cache_compact((pages,), table, refs)
+    with pytest.raises(ValueError, match="current device"):
+        ops.cache_copy((pages,), refs, refs)
