@@ -19,8 +19,10 @@ struct PagedParams {
   gemm_paged_attention_t a;
   int group;       // query heads a key head
   uint32_t group_inv;  // ceil(2^32 / group): x / group = umulhi(x, group_inv) for x, group < 2^16
-  // scale log2(e); with a softcap c: 2 log2(e) scale / c, and c log2(e)
-  float scale_log2, cap_in2, cap_out;
+  // scale log2(e); with a softcap c: scale / c, and c log2(e); with one of at
+  // most kCapShared (cap_shared) also 2 log2(e) scale / c
+  float scale_log2, cap_in, cap_out, cap_in2;
+  int cap_shared;
   int* status;
   // The kernel of 16 rows a block takes the sequences with at most
   // `few_rows` rows a key head; the tile kernel the others (tiled != 0).
@@ -40,7 +42,7 @@ struct PagedParams {
   int tile_parts;    // room for parts of items
   int box;           // keys a copy: the largest power of two that divides page_size, at most 128
   float* tile_part;  // per part 256 x D sums, 256 maxima, 256 sums (tile_splits > 1)
-  float s_scale;     // what makes a score of s: the scale's magnitude, or 2 c
+  float s_scale;     // what makes a score of s: the scale's magnitude, c, or 2 c with cap_shared
   int flip;          // a negative scale without a cap
   uint8_t* redo;     // per part and softmax warp: a result is not finite
   uint64_t wait_ns;
@@ -101,15 +103,26 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
+// The largest cap for which the kernels take tanh(x) as 1 - 2 / (e^{2x} + 1).
+// That cancels for small x and is off by some 2^-23, which the cap makes 2^-23
+// c of a score (a CPU emulation in fp32: 8e-6 with c = 50, 1e-3 with 10^4).  Up
+// to here that is 2^-17, of the order of the products' own error for scores
+// near the cap, and 64 times less than what the rounding of the weights to 16
+// bits costs.
+constexpr float kCapShared = 64.f;
+// A larger cap is none: a score would have to pass 2^88 for it to make a
+// difference in fp32 (c tanh(s / c) is s (1 - (s / c)^2 / 3 + ...)).
+constexpr float kCapNone = 0x1p100f;
+
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
-// scale s in units of log2, through the cap where there is one.  tanh(x) =
-// 1 - 2 / (e^{2x} + 1): the absolute error is that of a rounding near 1, of
-// which the cap makes c 2^-24, no more than the scores' own.
+// scale s in units of log2, through the cap where there is one.  (tanhf for
+// every cap took 66.5 us for 63.5 for one token in 64 sequences of 100 to 8300
+// keys, 12 heads of 128 over 2.)
 __device__ __forceinline__ float score_of(float s, const PagedParams& p) {
   if (p.cap_out == 0.f) return s * p.scale_log2;
-  const float e = exp2_approx(s * p.cap_in2);
-  return p.cap_out * (1.f - __fdividef(2.f, e + 1.f));
+  if (!p.cap_shared) return p.cap_out * tanhf(s * p.cap_in);
+  return p.cap_out * (1.f - __fdividef(2.f, exp2_approx(s * p.cap_in2) + 1.f));
 }
 
 // An item of the tile kernel: two 128-row tiles of a (sequence, key head) and

@@ -802,8 +802,11 @@ cudaError_t launch_paged_attention(const gemm_paged_attention_t& a, const PagedP
     p.tiles_per = (p.tiles_per + kWarps - 1) / kWarps * kWarps;
   p.units = a.sequences * a.kv_heads * p.row_tiles * p.splits;
   p.scale_log2 = a.scale * 1.4426950408889634f;
-  p.cap_in2 = a.softcap > 0.f ? 2.885390081777927f * (a.scale / a.softcap) : 0.f;
-  p.cap_out = a.softcap * 1.4426950408889634f;
+  const float cap = a.softcap <= kCapNone ? a.softcap : 0.f;
+  p.cap_in = cap > 0.f ? a.scale / cap : 0.f;
+  p.cap_out = cap * 1.4426950408889634f;
+  p.cap_shared = cap > 0.f && cap <= kCapShared;
+  p.cap_in2 = 2.885390081777927f * p.cap_in;
   char* at = static_cast<char*>(scratch);
   p.arrived = reinterpret_cast<int*>(at);
   p.queue = p.arrived + kPagedParts;
@@ -812,8 +815,10 @@ cudaError_t launch_paged_attention(const gemm_paged_attention_t& a, const PagedP
   if (plan.tiled) {
     p.tile_tokens = 128 / p.group;
     // (a scale of 0 as a tiny one, of which an infinity is still one)
-    p.s_scale = a.softcap > 0.f ? 2.f * p.cap_out : std::max(std::fabs(p.scale_log2), 1e-30f);
-    p.flip = a.softcap == 0.f && p.scale_log2 < 0.f;
+    p.s_scale = p.cap_shared ? 2.f * p.cap_out
+                : cap > 0.f  ? p.cap_out
+                             : std::max(std::fabs(p.scale_log2), 1e-30f);
+    p.flip = cap == 0.f && p.scale_log2 < 0.f;
     p.tile_splits = plan.tile_splits;
     p.tile_parts = static_cast<int>(plan.tile_parts);
     p.box = 16;

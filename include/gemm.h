@@ -493,6 +493,7 @@ gemm_status_t gemm_rotary(gemm_handle_t h, const gemm_rotary_t* a, void* stream)
  * j <= p = kv_lens[b] - n + i, and with window > 0 only those with
  * j > p - window.  Query head h reads key head h / (heads / kv_heads).
  *     s_j = scale * q . k_j, with softcap > 0: softcap * tanh(s_j / softcap)
+ *     (a softcap above 2^100 is none)
  *     out = sum_j softmax_j(s) v_j,   lse = log(sum_j exp(s_j))
  * A row that sees no key gives out = 0 and lse = -infinity.  Keys and values
  * that no row sees are not part of any result, whatever they hold.  Scores,

@@ -341,3 +341,36 @@ def test_a_handle_of_another_device_is_refused(h):
     assert lib.gemm_cache_fork(handle, c, 1, p, p, p, p, None) == host.INVALID
     assert lib.gemm_cache_compact(handle, c, p, None) == host.INVALID
     assert lib.gemm_cache_copy(handle, c, 1, p, p, None) == host.INVALID
+
+
+# ------------------------------------------------------------------- soft caps
+
+@pytest.mark.parametrize("lengths", [[(1, 700), (1, 5)], [(20, 333)], [(150, 903), (40, 41)]])
+@pytest.mark.parametrize("softcap", [0.5, 63.0, 65.0, 1e3, 1e4, 1e6, 1e8, 1e20, 1e30, 3e38])
+def test_attention_caps_of_any_size(h, lengths, softcap):
+    """A score through a cap is as exact as one without: the error grows with min(|s|, c), not with c.  With x = s / c
+    the tanh is off by 2^-21 of itself where its form does not cancel (two units of 2^-24 in its own value and as
+    many in x) and, up to a cap of 64, by 2^-21 c at most."""
+    c = Case(lengths, 4, 2, 128, 16, BF16, seed=18)
+    out, lse = c.run(h, softcap=softcap)
+    start = 0
+    for b, (n, length) in enumerate(lengths):
+        q = c.q[start:start + n].double().transpose(0, 1)
+        k, v = (t.double().transpose(0, 1).repeat_interleave(2, 0) for t in (c.keys[b], c.values[b]))
+        seen = torch.arange(length, device="cuda") <= length - n + torch.arange(n, device="cuda")[:, None]
+        s = q @ k.transpose(1, 2) / math.sqrt(128)
+        mag = (q.abs() @ k.abs().transpose(1, 2) / math.sqrt(128)).masked_fill(~seen, 0).amax(-1, keepdim=True)
+        s = softcap * torch.tanh(s / softcap)
+        form = 2.0 ** -21 * torch.minimum(mag, torch.tensor(float(softcap)).double()) if softcap > 64 else 2.0 ** -21 * softcap
+        delta = 2.0 ** -22 * (128 / 16 + 2) * mag + form + 2.0 ** -21
+        w = torch.softmax(s.masked_fill(~seen, -math.inf), -1)
+        ref, scale_w = w @ v, w @ v.abs()
+        ref_lse = torch.logsumexp(s.masked_fill(~seen, -math.inf), -1)
+        bound = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 4 * delta + 2.0 ** -20) * scale_w + 2.0 ** -24
+        err = (out[start:start + n].double().transpose(0, 1) - ref).abs()
+        assert bool((err <= bound).all()), (b, float((err / bound).max()))
+        err = (lse[start:start + n].double().transpose(0, 1) - ref_lse).abs()
+        bound = 2 * delta[..., 0] + 2.0 ** -21 * (1 + ref_lse.abs())
+        assert bool((err <= bound).all()), (b, "lse", float((err / bound).max()))
+        start += n
+    assert h.check_device() == 0
