@@ -536,15 +536,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
             for (int t = 0; t < 64; ++t) s[t] ^= 0x80000000u;
           }
-          // Capped scores are masked before, too: what an unseen slot holds
-          // would reach the scores that share its reciprocal.
+          // Capped scores are masked before, too, with zeros: what an unseen
+          // slot holds would reach the scores that share its reciprocal (and
+          // so would an infinity, which a scale of 0 makes a NaN).
 #pragma unroll 1
           for (bool capped = p.cap_out == 0.f;; capped = true) {
             if (!whole) {
               // this row sees the keys [hi - window, hi)
               const int from = a.window > 0 ? hi - a.window - key0 : 0, to = hi - key0;
+              const uint32_t unseen = capped ? 0xff800000u : 0u;
 #pragma unroll
-              for (int t = 0; t < 64; ++t) s[t] = t >= from && t < to ? s[t] : 0xff800000u;
+              for (int t = 0; t < 64; ++t) s[t] = t >= from && t < to ? s[t] : unseen;
             }
             if (capped) break;
             if constexpr (FAR)

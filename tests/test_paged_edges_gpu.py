@@ -374,3 +374,23 @@ def test_attention_caps_of_any_size(h, lengths, softcap):
         assert bool((err <= bound).all()), (b, "lse", float((err / bound).max()))
         start += n
     assert h.check_device() == 0
+
+
+def test_attention_capped_with_a_scale_of_zero(h):
+    """All scores are 0: every row is the mean of what it sees, in the time of any other scale.  (The mean of numbers
+    that the products take exactly: only the sums, 2^-20, and the result are rounded.)"""
+    c = Case([(1000, 3000)], 16, 2, 128, 16, BF16, seed=4)
+    time = {}
+    for scale in (0.0, 0.1):
+        for _ in range(3):
+            out, lse = c.run(h, softcap=30.0, scale=scale)
+        began, ended = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        began.record()
+        for _ in range(5):
+            c.run(h, softcap=30.0, scale=scale)
+        ended.record()
+        torch.cuda.synchronize()
+        time[scale] = began.elapsed_time(ended)
+    assert time[0.0] < 3 * time[0.1], time
+    c.check(*c.run(h, softcap=30.0, scale=0.0), 0.0, 30.0)
+    assert h.check_device() == 0
