@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
   }
   if constexpr (TILED) {
     grid_dep_wait();
-    const int64_t parts = min(p.queue[2], p.tile_parts);
+    const int64_t parts = p.queue[2];
     if (p.tile_splits > 1) {
       constexpr int kUnits = 256 / kRows;
       const int units = static_cast<int>(parts / p.tile_splits) * kUnits;

@@ -308,16 +308,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int boxes = kKeysBlock / p.box;
     uint32_t n = 0, items = 0, tails = 0;  // blocks, items, blocks with zeros so far
     uint32_t filled[2] = {0, 0};           // stages of K and V filled
+    int computed = 0;                      // items of the call, none after a wait that ran out
     bool ok = true;
     for (int k = 0; ok; ++k) {
       const PagedItem it = item_at(k);
       if (!it.valid) {
-        // how many items there are, for the kernel that ends after this one
-        if (lane == 0 && blockIdx.x == 0) p.queue[2] = it.part;
+        computed = min(it.part, p.tile_parts);
         break;
       }
-      if (it.part >= p.tile_parts) {
+      if (it.part >= p.tile_parts) {  // only where the sequences' offsets are out of order
         if (lane == 0) atomicExch(p.status, kDevBadIndex);
+        computed = p.tile_parts;
         break;
       }
       const Blocks b = blocks_of(p, it);
@@ -403,6 +404,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         there = next_there;
       }
     }
+    // how many there are to join, for the kernel that ends after this one
+    if (lane == 0 && blockIdx.x == 0) p.queue[2] = computed;
     // every copy lands before the block exits: the last use of each stage
     if (lane == 0) {
       if (items > 0) drain_wait(q_full, (items - 1) & 1u, p.status, p.wait_ns);

@@ -394,3 +394,22 @@ def test_attention_capped_with_a_scale_of_zero(h):
     assert time[0.0] < 3 * time[0.1], time
     c.check(*c.run(h, softcap=30.0, scale=0.0), 0.0, 30.0)
     assert h.check_device() == 0
+
+
+def test_attention_offsets_out_of_order_leave_the_other_sequences(h):
+    """Overlapping ranges of tokens with offsets out of order between them: more work than the call has room for is
+    reported and left out, what comes before it is right, whatever the call before had."""
+    small = Case([(40, 60)], 4, 2, 128, 16, BF16, seed=1)
+    c = Case([(100, 3000)] + [(1000, 1000)], 4, 2, 128, 16, BF16, seed=2)
+    table = torch.cat([c.table[:1]] + [c.table[1:]] * 31)
+    lens = torch.cat([c.lens[:1]] + [c.lens[1:]] * 31)
+    cu = _i32([0, 100] + [1100, 100] * 15 + [1100])
+    assert cu.numel() == table.shape[0] + 1
+    small.run(h)
+    out, lse = h.paged_attention(c.q, c.k, c.v, table, lens, cu_q=cu, max_q=1000, return_lse=True)
+    assert h.check_device() == 8
+    assert h.plan()["split_k"] > 1
+    first = Case.__new__(Case)
+    first.__dict__.update(c.__dict__)
+    first.lengths, first.keys, first.values, first.q = c.lengths[:1], c.keys[:1], c.values[:1], c.q[:100]
+    first.check(out[:100], lse[:100])
