@@ -227,7 +227,7 @@ constexpr int kScratchBlocks = 24;
 // kernel, flags and at most kPagedTileParts partial results of 256 rows.
 constexpr int kPagedPartRows = 16;
 constexpr int64_t kPagedParts = 2048, kPagedTileParts = 1024;
-constexpr int64_t kPagedMostSplits = 256;  // parts of one range: their weights fit the 16-row kernel's ring
+constexpr int64_t kPagedMostSplits = 256;  // parts of one range or item: their weights fit the 16-row kernel's ring
 constexpr size_t kPagedRowScratch =
     (kPagedParts + 64) * sizeof(int) + kPagedParts * kPagedPartRows * (128 + 2) * sizeof(float);
 struct PagedPlan {

@@ -50,6 +50,8 @@ constexpr int kKeys = 16;              // keys a warp's tile
 // call's blocks at once (paged_attention_plan).
 constexpr int kStages = 2, kDeepStages = 4;
 constexpr int ring_bytes(int dim, int stages) { return kWarps * stages * 2 * kKeys * dim * 2; }
+// The joins keep the maxima (then weights) and sums of a range's parts there.
+static_assert(kPagedMostSplits * kRows * 2 * static_cast<int>(sizeof(float)) <= ring_bytes(64, kStages));
 // Sequences with more rows a key head go to the tile kernel.  With 30 rows the
 // 16-row one is ahead (10.8 against 14.0 us over 500 keys, 19.5 against 23.7 us
 // in 16 sequences of 2000), with 60 rows behind (28.3 against 24.5 us).
@@ -751,7 +753,8 @@ PagedPlan paged_attention_plan(const gemm_paged_attention_t& a, int sms) {
   // own: 7 chunks of 320 tokens, 12 heads, against 7600 keys, 168 items, took
   // 322 us whole and 248 in three parts; 3 of 400, 16 heads over 4, against
   // 2000 keys, 84 items, 69 us in two parts, 65 in three and 43 whole.
-  const int64_t most_parts = std::max<int64_t>(1, std::min<int64_t>(blocks / 4, kPagedTileParts / most));
+  const int64_t most_parts =
+      std::max<int64_t>(1, std::min({blocks / 4, kPagedTileParts / most, kPagedMostSplits}));
   auto cost = [&](int64_t n) { return (items * n + sms - 1) / sms * ((blocks + n - 1) / n + 5); };
   int64_t parts = 1;
   for (int64_t rounds = 1; rounds <= 8; ++rounds) {
