@@ -11,11 +11,13 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <exception>
 #include <optional>
 #include <string>
 
@@ -226,8 +228,8 @@ PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n, Py_ssize_t wan
   } catch (const Refused& r) {
     PyErr_SetString(r.type, r.what.c_str());
   } catch (const Raised&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {  // torch's own, as torch raises them (memory that could not be had among them)
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

@@ -413,3 +413,12 @@ def test_attention_offsets_out_of_order_leave_the_other_sequences(h):
     first.__dict__.update(c.__dict__)
     first.lengths, first.keys, first.values, first.q = c.lengths[:1], c.keys[:1], c.values[:1], c.q[:100]
     first.check(out[:100], lse[:100])
+
+
+def test_out_of_memory_is_torch_s_own_error(h):
+    q = torch.zeros(1, 1, 64, device="cuda").expand(2 ** 24, 2 ** 10, 64)  # 4 TiB of output
+    freqs, _ = dg.rotary_frequencies(64, device="cuda")
+    positions = torch.zeros(2 ** 24, dtype=torch.int64, device="cuda")
+    with pytest.raises(torch.cuda.OutOfMemoryError):
+        h.rotary(q, None, positions, freqs)
+    assert h.check_device() == 0
