@@ -128,7 +128,8 @@ struct IdxShared {
 };
 
 // Lists the free pages (and with `live` the used ones) of this block's
-// segment, ascending; returns true in the block that finishes last, with the
+// segment, ascending, and with `live` gives the free ones no place in ws.map;
+// returns true in the block that finishes last, with the
 // segments' ranks in sh.free_at / live_at.
 __device__ bool list_pages(const PageState& st, const Scratch& ws, IdxShared& sh, bool live) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -165,7 +166,10 @@ __device__ bool list_pages(const PageState& st, const Scratch& ws, IdxShared& sh
     for (int u = 0; u < kIdxBatch; ++u) {
       const int rank = before + (warp > 0 ? sh.cnt[u][warp - 1] : 0) + __popc(m[u] & ((1u << lane) - 1u));
       const int64_t i = base + u * kIdxThreads + threadIdx.x;
-      if (r[u] == 0) ws.free_list[first + n_free + rank] = static_cast<int32_t>(i);
+      if (r[u] == 0) {
+        ws.free_list[first + n_free + rank] = static_cast<int32_t>(i);
+        if (live) ws.map[i] = -1;
+      }
       if (live && r[u] != 0 && i < end) ws.live_list[first + n_live + static_cast<int>(i - base) - rank] = static_cast<int32_t>(i);
       before += sh.cnt[u][kIdxWarps - 1];
     }
@@ -586,14 +590,14 @@ __global__ void __launch_bounds__(kCopyThreads)
   for (int64_t e = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x; e < entries; e += threads) {
     int32_t* entry = st.table + e / st.width * st.table_row + e % st.width;
     const int page = *entry;
-    if (page >= st.pages) {
-      atomicExch(st.status, kDevBadIndex);
-    } else if (page >= live) {
-      // in use (a table holds it), so it moved; a page that refs calls free
-      // has no new place
-      const int to = st.refs[page] == 0 ? ws.map[page] : page;
+    if (page < live) continue;  // stays (or -1)
+    // in use, as a table holds it, and so moved; a page that refs calls free
+    // has no new place
+    const int to = page < st.pages ? ws.map[page] : -1;
+    if (to >= 0)
       *entry = to;
-    }
+    else
+      atomicExch(st.status, kDevBadIndex);
   }
   copy_pairs(p, static_cast<int64_t>(blockIdx.x) * (kCopyThreads / 32) + (threadIdx.x >> 5),
              static_cast<int64_t>(gridDim.x) * (kCopyThreads / 32));

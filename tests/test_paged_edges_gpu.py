@@ -422,3 +422,26 @@ def test_out_of_memory_is_torch_s_own_error(h):
     with pytest.raises(torch.cuda.OutOfMemoryError):
         h.rotary(q, None, positions, freqs)
     assert h.check_device() == 0
+
+
+# ------------------------------------------------------------------- pages
+
+# ------------------------------------------------------------ tables that are wrong
+
+def test_compact_leaves_an_entry_of_a_free_page(h):
+    """A table entry that names a page which refs calls free has no new place: reported, and left as it is."""
+    table, lens, refs = _cache(3, 4, 40)
+    pool = torch.arange(40, dtype=torch.int32, device="cuda").view(40, 1).repeat(1, 4)
+    # scratch words of earlier calls
+    h.cache_grow(table, lens, refs, 16, _i32([0, 1, 2]), _i32([64, 64, 64]), 192)
+    h.cache_shrink(table, lens, refs, 16, _i32([0]))
+    h.cache_compact((pool,), table, refs)
+    table.fill_(-1), lens.zero_(), refs.zero_()
+    refs[30], refs[35] = 1, 2
+    table[0, 0], table[1, 0], table[2, 0] = 30, 35, 35
+    table[2, 1] = 33  # free
+    table[1, 1] = 10 ** 6
+    info = h.cache_compact((pool,), table, refs)
+    assert info.tolist() == [2, 2]
+    assert table[:, :2].tolist() == [[0, -1], [1, 10 ** 6], [1, 33]]
+    assert h.check_device() == 8
