@@ -44,7 +44,7 @@ struct Scratch {
   int32_t* free_list;  // segment s's free pages, ascending, from s * seg on
   int32_t* live_list;  // and its pages in use
   int32_t *src, *dst;  // pairs of pages to copy
-  int32_t* map;        // compact: new place of the page that moves
+  int32_t* map;        // compact: new place of a page that moves, -1 for a free one
   int32_t *at, *before, *token;  // per sequence of the call: first rank, length, first token
 };
 
@@ -96,21 +96,21 @@ int idx_blocks(const PageState& s) { return std::max(1, (s.pages + s.seg - 1) / 
 
 // Inclusive sum over the block; `part` holds kIdxWarps values.  The total is
 // in *total for every thread.
-__device__ __forceinline__ int block_scan(int v, int* part, int* total) {
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, v, d);
+    const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
     if (lane >= d) v += o;
   }
   __syncthreads();  // the previous use of `part`
   if (lane == 31) part[warp] = v;
   __syncthreads();
   if (warp == 0) {
-    int w = part[lane];
+    int64_t w = part[lane];
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, w, d);
+      const int64_t o = __shfl_up_sync(0xffffffffu, w, d);
       if (lane >= d) w += o;
     }
     part[lane] = w;
@@ -121,7 +121,7 @@ __device__ __forceinline__ int block_scan(int v, int* part, int* total) {
 }
 
 struct IdxShared {
-  int part[kIdxWarps];
+  int64_t part[kIdxWarps];
   int cnt[kIdxBatch][kIdxWarps];
   int free_at[kIdxBlocks + 1], live_at[kIdxBlocks + 1];  // ranks of the segments' first pages
   int last;
@@ -253,10 +253,12 @@ __global__ void __launch_bounds__(kIdxThreads)
   grid_dep_launch();
   if (!list_pages(st, ws, sh, false)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int need = 0, refused = 0, token = 0;  // totals so far
+  int64_t need = 0, token = 0;  // totals so far
+  int refused = 0;
   for (int base = 0; base < n; base += kIdxThreads) {
     const int i = base + threadIdx.x;
-    int take = 0, add = 0, no = 0, before = 0;
+    int64_t take = 0;
+    int add = 0, no = 0, before = 0;
     if (i < n) {
       const int seq = seqs[i];
       add = counts[i];
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kIdxThreads)
         before = length_of(st, seq);
         const int64_t after = static_cast<int64_t>(before) + add;
         if (after > static_cast<int64_t>(st.width) * st.page_size) no = 1;
-        take = static_cast<int>((after + st.page_size - 1) / st.page_size) - pages_for(before, st.page_size);
+        take = (after + st.page_size - 1) / st.page_size - pages_for(before, st.page_size);
         if (add > 0 && before % st.page_size != 0) {
           const int page = checked_page(st, st.table[seq * st.table_row + before / st.page_size]);
           if (page >= 0 && st.refs[page] > 1) {
@@ -284,29 +286,25 @@ __global__ void __launch_bounds__(kIdxThreads)
         no = 1;
       }
     }
-    int sum;
-    int incl = block_scan(take, sh.part, &sum);
+    int64_t sum;
+    int64_t incl = block_scan(take, sh.part, &sum);
     if (i < n) {
-      ws.at[i] = need + incl - take;
+      ws.at[i] = static_cast<int32_t>(need + incl - take);  // (read where all of them are there)
       ws.before[i] = before;
     }
     need += sum;
     incl = block_scan(add, sh.part, &sum);
-    if (i < n) ws.token[i] = token + incl - add;
+    if (i < n) ws.token[i] = static_cast<int32_t>(min(token + incl - add, static_cast<int64_t>(INT32_MAX)));
     token += sum;
-    block_scan(no, sh.part, &sum);
-    refused += sum;
+    refused += __syncthreads_count(no);
   }
-  const int free_pages = sh.free_at[gridDim.x];
-  const int missing = max(0, need - free_pages);
+  const int64_t missing = max(static_cast<int64_t>(0), need - sh.free_at[gridDim.x]);
   const bool ok = missing == 0 && refused == 0;
   if (threadIdx.x == 0) {
-    info[0] = ok ? need : 0;
-    info[1] = missing;
+    info[0] = ok ? static_cast<int32_t>(need) : 0;
+    info[1] = static_cast<int32_t>(min(missing, static_cast<int64_t>(INT32_MAX)));
     info[2] = refused;
     if (tokens != token) atomicExch(st.status, kDevBadIndex);
-  }
-  if (threadIdx.x == 0) {
     moves = 0;
     if (!ok) ws.head->moves = 0;
   }
@@ -322,9 +320,9 @@ __global__ void __launch_bounds__(kIdxThreads)
         }
         const int own = ws.before[lo] < 0 ? 1 : 0;
         const int before = own ? ~ws.before[lo] : ws.before[lo];
-        const int pos = before + (t - ws.token[lo]);
-        position = pos;
+        position = static_cast<int64_t>(before) + (t - ws.token[lo]);
         if (ok) {
+          const int pos = static_cast<int>(position);
           const int j = pos / st.page_size, held = pages_for(before, st.page_size) - own;
           const int page = j < held ? checked_page(st, st.table[seqs[lo] * st.table_row + j])
                                     : page_of(ws.free_list, sh.free_at, st.seg, ws.at[lo] + j - held);
@@ -412,15 +410,14 @@ __global__ void __launch_bounds__(kIdxThreads)
         no = 1;
       }
     }
-    int sum;
-    const int incl = block_scan(take, sh.part, &sum);
+    int64_t sum;
+    const int64_t incl = block_scan(take, sh.part, &sum);
     if (i < n) {
-      ws.at[i] = take ? need + incl - 1 : -1;
+      ws.at[i] = take ? need + static_cast<int>(incl) - 1 : -1;
       ws.before[i] = len;
     }
-    need += sum;
-    block_scan(no, sh.part, &sum);
-    refused += sum;
+    need += static_cast<int>(sum);
+    refused += __syncthreads_count(no);
   }
   const int missing = max(0, need - sh.free_at[gridDim.x]);
   const bool ok = missing == 0 && refused == 0;

@@ -445,3 +445,20 @@ def test_compact_leaves_an_entry_of_a_free_page(h):
     assert info.tolist() == [2, 2]
     assert table[:, :2].tolist() == [[0, -1], [1, 10 ** 6], [1, 33]]
     assert h.check_device() == 8
+
+
+def test_grow_totals_beyond_32_bits(h):
+    """More pages wanted than an int counts (by rows that are one row, repeated): missing, and nothing changed."""
+    width = 2 ** 31 - 2 ** 17
+    row = torch.empty(1, width, dtype=torch.int32, device="cuda")
+    row[0, :8] = -1
+    table = row.expand(6, width)
+    lens, refs = torch.zeros(6, dtype=torch.int32, device="cuda"), torch.zeros(5000, dtype=torch.int32, device="cuda")
+    for counts in ([1_500_000_000] * 2, [1_500_000_000] * 3, [2_000_000_000] * 6, [1, 2_000_000_000, 2_000_000_000]):
+        seqs = list(range(len(counts)))
+        positions, slots, info = h.cache_grow(table, lens, refs, 1, _i32(seqs), _i32(counts), 4)
+        assert info.tolist() == [0, min(sum(counts) - 5000, 2 ** 31 - 1), 0] and slots.tolist() == [-1] * 4
+        assert h.check_device() == 8  # `tokens` is not the sum of the counts
+    assert int(lens.abs().sum()) == 0 and int(refs.abs().sum()) == 0
+    del row, table
+    torch.cuda.empty_cache()
