@@ -46,10 +46,11 @@ gemm_status_t check_rotary(const gemm_rotary_t& a) {
   if (!std::isfinite(a.amplitude)) return GEMM_ERR_INVALID_VALUE;
   if (a.rotary_dim > 0 && a.position_bytes != 4 && a.position_bytes != 8) return GEMM_ERR_INVALID_VALUE;
   const bool paged = a.page_size > 0;
-  if (paged && (a.k == nullptr || a.v == nullptr || a.num_pages < 0 || a.num_pages > kMaxPages))
-    return GEMM_ERR_INVALID_VALUE;
+  if (paged && (a.num_pages < 0 || a.num_pages > kMaxPages)) return GEMM_ERR_INVALID_VALUE;
+  if (a.tokens == 0) return GEMM_OK;  // (a tensor without elements has no address)
+  if (paged && (a.k == nullptr || a.v == nullptr)) return GEMM_ERR_INVALID_VALUE;
   if (!paged && a.v != nullptr) return GEMM_ERR_INVALID_VALUE;
-  if (a.tokens == 0 || (a.heads == 0 && (a.k == nullptr || a.kv_heads == 0))) return GEMM_OK;
+  if (a.heads == 0 && (a.k == nullptr || a.kv_heads == 0)) return GEMM_OK;
   if (a.heads > 0 && (a.q == nullptr || a.q_out == nullptr)) return GEMM_ERR_INVALID_VALUE;
   if (a.k != nullptr && a.k_out == nullptr) return GEMM_ERR_INVALID_VALUE;
   if (paged && (a.v_out == nullptr || a.slots == nullptr)) return GEMM_ERR_INVALID_VALUE;

@@ -462,3 +462,14 @@ def test_grow_totals_beyond_32_bits(h):
     assert int(lens.abs().sum()) == 0 and int(refs.abs().sum()) == 0
     del row, table
     torch.cuda.empty_cache()
+
+
+def test_append_of_no_tokens(h):
+    """Nothing to append is no error, as nothing to rotate is not."""
+    x = torch.empty(0, 4, 64, device="cuda")
+    pools = [torch.ones(2, 16, 4, 64, dtype=BF16, device="cuda") for _ in range(2)]
+    none = torch.empty(0, dtype=torch.int64, device="cuda")
+    freqs, _ = dg.rotary_frequencies(64, device="cuda")
+    assert h.rotary_append(x, x, x, none, none, *pools, freqs).shape == x.shape
+    assert h.rotary_append(x, x, x, None, none, *pools).dtype == BF16
+    assert all(bool((p == 1).all()) for p in pools) and h.check_device() == 0

@@ -4,7 +4,7 @@ import torch
 
 import dense_gemm_transformer_gb300 as dg
 from dense_gemm_transformer_gb300 import paged
-from tests.test_paged_host import H, INVALID, MISALIGNED, P, _cache
+from tests.test_paged_host import H, INVALID, MISALIGNED, OK, P, ROTARY, _cache, _pack
 
 
 @pytest.fixture(scope="module")
@@ -59,3 +59,11 @@ def test_tensors_of_another_device_are_refused(lib):
         ops.cache_compact((pages,), table, refs)
     with pytest.raises(ValueError, match="current device"):
         ops.cache_copy((pages,), refs, refs)
+
+
+def test_nothing_to_append_is_no_error(lib):
+    """Tensors without elements have no address."""
+    none = dict(tokens=0, q=0, k=0, v=0, q_out=0, positions=0, slots=0)
+    assert lib.gemm_rotary(H, _pack("gemm_rotary_t", {**ROTARY, **none}), None) == OK
+    assert lib.gemm_rotary(H, _pack("gemm_rotary_t", {**ROTARY, **none, "head_dim": 127}), None) == INVALID
+    assert lib.gemm_rotary(H, _pack("gemm_rotary_t", {**ROTARY, **none, "num_pages": -1}), None) == INVALID
