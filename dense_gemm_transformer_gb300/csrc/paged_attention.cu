@@ -124,7 +124,7 @@ __device__ __forceinline__ void rows_unit(const PagedParams& p, uint8_t* smem, R
   // Keys row r sees: [lo(r), hi(r)).
   const int seen0 = s.len - s.n + token0 + 1;
   auto hi_of = [&](int r) { return max(0, seen0 + by_group(p, head0 + r)); };
-  auto lo_of = [&](int r) { return a.window > 0 ? max(0, seen0 + by_group(p, head0 + r) - a.window) : 0; };
+  auto lo_of = [&](int r) { return a.window > 0 ? max(0, hi_of(r) - a.window) : 0; };
   const int lo = lo_of(0), hi = hi_of(rows - 1);
   // keys every row sees; in a tile without others of [lo, hi), all rows see
   // the same

@@ -212,7 +212,7 @@ __device__ __forceinline__ Blocks blocks_of(const PagedParams& p, const PagedIte
   const int t1 = min(t0 + 2 * p.tile_tokens, it.s.n);
   const int before = it.s.len - it.s.n;  // keys before the first new token
   b.hi = max(0, before + t1);
-  b.lo = p.a.window > 0 ? max(0, before + t0 + 1 - p.a.window) : 0;
+  b.lo = p.a.window > 0 ? max(0, max(0, before + t0 + 1) - p.a.window) : 0;
   const int k0 = b.lo / kKeysBlock, k1 = b.hi > b.lo ? (b.hi + kKeysBlock - 1) / kKeysBlock : k0;
   const int per = (k1 - k0 + p.tile_splits - 1) / p.tile_splits;
   b.first = min(k1, k0 + it.split * per);

@@ -473,3 +473,15 @@ def test_append_of_no_tokens(h):
     assert h.rotary_append(x, x, x, none, none, *pools, freqs).shape == x.shape
     assert h.rotary_append(x, x, x, None, none, *pools).dtype == BF16
     assert all(bool((p == 1).all()) for p in pools) and h.check_device() == 0
+
+
+# --------------------------------------------- windows, values and small weights
+
+@pytest.mark.parametrize("n,length", [(1, 5), (4, 1), (30, 10), (200, 60), (5, 300)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 100, 2 ** 30])
+def test_attention_windows_beyond_every_key(h, n, length, window):
+    """A window that no sequence fills is none, also where there are more new tokens than keys."""
+    c = Case([(n, length), (1, 40)], 4, 2, 64, 16, BF16, seed=13)
+    out, lse = c.run(h, window=window)
+    c.check(out, lse, None, 0.0, 0)
+    assert h.check_device() == 0
