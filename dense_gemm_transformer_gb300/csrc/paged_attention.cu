@@ -96,6 +96,13 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The largest weight is 2^kBias, here and in the sums, and the factor cancels
+// in the output.  In fp16 numbers below 2^-14 have fewer bits: with 1 for the
+// largest, a quarter of a million keys with weights of 2^-18 each that a warp
+// meets beside a few of 1 had their part off by 2^-7 of itself.
+template <typename T>
+constexpr float kBias = std::is_same_v<T, __half> ? 14.f : 0.f;
+
 struct RowsShared {
   float m[kWarps][kRows], l[kWarps][kRows];
   float f[kWarps][kRows];  // factors of the warps' sums
@@ -248,8 +255,9 @@ __device__ __forceinline__ void rows_unit(const PagedParams& p, uint8_t* smem, R
       top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], 2));
       const float next = fmaxf(m[u], top[u]);
       raised |= next > m[u];
-      shift[u] = next == neg_inf() ? 0.f : next;  // a row that has seen no key yet: its scores are all -inf
-      alpha[u] = exp2_approx(m[u] - shift[u]);    // 0 for the first key seen
+      const float from = next == neg_inf() ? 0.f : next;  // a row that has seen no key yet: its scores are all -inf
+      alpha[u] = exp2_approx(m[u] - from);                // 0 for the first key seen
+      shift[u] = from - kBias<T>;
       m[u] = next;
     }
     if (__any_sync(0xffffffffu, raised)) {
@@ -273,7 +281,8 @@ __device__ __forceinline__ void rows_unit(const PagedParams& p, uint8_t* smem, R
     if (max(key0, lo) >= common_lo && min(key0 + kKeys, hi) <= common_hi) {
       // The weights as the A operand, as a sum of two 16-bit numbers: one
       // would cost as much accuracy as the output's own rounding, and the
-      // second product is free here.
+      // second product is free here.  (2^14 is in range, and so is what the
+      // rounding leaves.)
       uint32_t ph[4], pl[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -331,7 +340,7 @@ __device__ __forceinline__ void rows_unit(const PagedParams& p, uint8_t* smem, R
     l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
     l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
     if (quad == 0) {
-      sh.m[warp][g + 8 * u] = m[u];
+      sh.m[warp][g + 8 * u] = m[u] - kBias<T>;
       sh.l[warp][g + 8 * u] = l[u];
     }
   }

@@ -485,3 +485,29 @@ def test_attention_windows_beyond_every_key(h, n, length, window):
     out, lse = c.run(h, window=window)
     c.check(out, lse, None, 0.0, 0)
     assert h.check_device() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_attention_many_small_weights(h, dtype):
+    """Four keys far above a million others, whose weights of 2^-18 1.0078 each add up to as much: fp16 has no more
+    than 8 bits for such a number.  So many sequences (of the same pages) that none is split, and the four where each
+    warp of a block meets one."""
+    dim, page, length, sequences = 64, 128, 2 ** 20, 1216
+    k = torch.zeros(length // page, page, 1, dim, dtype=dtype, device="cuda")
+    v = torch.ones_like(k)
+    q = torch.zeros(sequences, 1, dim, dtype=dtype, device="cuda")
+    q[..., 0] = 1.0
+    k[0, 0:64:16, :, 0] = 1.0
+    v[0, 0:64:16] = 0.0
+    scale = (18 - math.log2(1.0078)) * math.log(2)
+    table = torch.arange(length // page, dtype=torch.int32, device="cuda")[None].expand(sequences, -1)
+    lens = torch.full((sequences,), length, dtype=torch.int32, device="cuda")
+    out, lse = h.paged_attention(q, k, v, table, lens, scale=scale, return_lse=True)
+    assert h.plan()["split_k"] == 1
+    others = (length - 4) * math.exp(-scale)
+    want = others / (4 + others)
+    # the scale as an fp32 (2^-25 of 12.5) and the weights' function, 2^-20; the sums of a warp's quarter million keys,
+    # 16 a product, at most 2^14 steps of 2^-24 (and half as much on average); the output's own rounding
+    assert float((out.double() - want).abs().max()) <= want * (torch.finfo(dtype).eps / 2 + 2.0 ** -10)
+    assert abs(float(lse[0, 0]) - (scale + math.log(4 + others))) <= 2.0 ** -10
+    assert h.check_device() == 0
