@@ -110,6 +110,48 @@ struct RowsShared {
   int last, unit;
 };
 
+// The sums of a warp that are not numbers though the scores are (lsum: the
+// rows' sums of weights): a value that a row sees is infinite or not a number.
+// Of a weight's two 16-bit numbers one may be 0 or negative, and the sum of
+// their products with an infinity NaN; which infinity it should be is found
+// from the values.  Not inlined: its registers are the kernel's otherwise, and
+// those decide how many blocks an SM has.
+template <typename T, int D>
+__device__ __noinline__ void infinite_sums(const PagedParams& p, float* sums, const float* lsum, const int32_t* table,
+                                           const T* vbase, int rows, int head0, int seen0, int tile, int tiles) {
+  const gemm_paged_attention_t& a = p.a;
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int r = 0; r < rows; ++r) {
+    float* row = sums + r * D;
+    const int swap = 8 * (r & 3);
+    bool open = false;
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) open |= isnan(row[(32 * x + lane) ^ swap]);
+    if (!__any_sync(0xffffffffu, open) || isnan(lsum[r])) continue;
+    const int to = max(0, seen0 + by_group(p, head0 + r)), from = a.window > 0 ? max(0, to - a.window) : 0;
+    int kinds[D / 32] = {};  // 1: infinity, 2: minus infinity, 4: not a number
+#pragma unroll 1
+    for (int it = 0; it < tiles; ++it) {
+      const int key0 = (tile + it * kWarps) * kKeys, col = key0 / a.page_size;
+      if (key0 + kKeys <= from || key0 >= to) continue;
+      const int page = table[col];
+      if (page < 0 || page >= a.num_pages) continue;
+      const T* v = vbase + page * a.v_page + (key0 - col * a.page_size) * a.v_slot + lane;
+#pragma unroll 1
+      for (int key = max(key0, from); key < min(key0 + kKeys, to); ++key)
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+          const float y = as_f(v[(key - key0) * a.v_slot + 32 * x]);
+          if (!isfinite(y)) kinds[x] |= isnan(y) ? 4 : y > 0.f ? 1 : 2;
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x)
+      if (kinds[x] == 1 || kinds[x] == 2) row[(32 * x + lane) ^ swap] = kinds[x] == 1 ? -neg_inf() : neg_inf();
+  }
+}
+
 // The rows row0 .. row0 + rows - 1 of a (sequence, key head), all of their
 // keys or (of `splits` parts) part `split`.  `range` numbers the rows among
 // the call's ranges of parts.  ahead_page: the table's entry ahead_col, read
@@ -335,8 +377,13 @@ __device__ __forceinline__ void rows_unit(const PagedParams& p, uint8_t* smem, R
     __syncwarp();  // the tile's slot is filled again
   }
   cp_async_wait<0>();
+  bool nan = false;  // a sum of these rows
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
+    float sum = 0.f;
+#pragma unroll
+    for (int d = 0; d < D / 8; ++d) sum += o[d][2 * u] + o[d][2 * u + 1];
+    nan |= g + 8 * u < rows && isnan(sum);
     l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
     l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
     if (quad == 0) {
@@ -355,6 +402,10 @@ __device__ __forceinline__ void rows_unit(const PagedParams& p, uint8_t* smem, R
       const int r = g + 8 * u, c = (8 * d + 2 * quad) ^ (8 * (r & 3));
       *reinterpret_cast<float2*>(mine_o + r * D + c) = make_float2(o[d][2 * u], o[d][2 * u + 1]);
     }
+  if (__any_sync(0xffffffffu, nan)) {
+    __syncwarp();
+    infinite_sums<T, D>(p, mine_o, sh.l[warp], table, vbase, rows, head0, seen0, tile0 + begin + warp, mine);
+  }
   __syncthreads();
 
   // Joins the warps: a thread per row weighs their sums, then every thread
@@ -601,8 +652,11 @@ __device__ __forceinline__ void take_unit(const PagedParams& p, uint8_t* smem, R
                     split, p.splits, range, ahead_col, ahead_page);
 }
 
+// (Three blocks an SM with heads of 128, as paged_attention_plan counts on: the
+// compiler takes 230 registers by itself, and 4 sequences of 32000 keys 39 us
+// for 33.)
 template <typename T, int D, bool TILED>
-__global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(kThreads, D == 128 && !TILED ? 3 : 0) paged_rows_kernel(const __grid_constant__ PagedParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ RowsShared sh;
   // Beside the tile kernel, this one starts when all of that one's blocks

@@ -511,3 +511,35 @@ def test_attention_many_small_weights(h, dtype):
     assert float((out.double() - want).abs().max()) <= want * (torch.finfo(dtype).eps / 2 + 2.0 ** -10)
     assert abs(float(lse[0, 0]) - (scale + math.log(4 + others))) <= 2.0 ** -10
     assert h.check_device() == 0
+
+
+# --------------------------------------------- values, windows and other ends
+
+@pytest.mark.parametrize("n,length", [(1, 1), (1, 700), (3, 60), (20, 333), (40, 300), (150, 400)])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_attention_infinite_values_give_infinities(h, n, length, dtype):
+    """A value of infinity that a row sees, with a weight above 0, makes its output that infinity, and one of each
+    sign not a number; the other columns and heads are as they are without."""
+    c = Case([(n, length)], 4, 2, 64, 16, dtype, seed=31)
+    at = max(0, length - n - 2)  # seen by every row
+    v = c.values[0][at].clone()
+    clean, lse_clean = c.run(h)
+    v[0, 3], v[0, 7] = math.inf, -math.inf
+    c.put(0, at, v=v)
+    out, lse = c.run(h)
+    assert bool((out[:, :2, 3] == math.inf).all()) and bool((out[:, :2, 7] == -math.inf).all())
+    rest = torch.ones(64, dtype=torch.bool, device="cuda")
+    rest[[3, 7]] = False
+    ref, bound, _, _ = next(c.reference(dtype))
+    err = (out.double().transpose(0, 1) - ref).abs()
+    assert bool((err <= bound)[:, :, rest].all())
+    assert torch.equal(out[:, 2:], clean[:, 2:])
+    if length > 4:
+        v[0, 3] = math.inf
+        c.put(0, at, v=v)
+        other = c.values[0][at - 1].clone()
+        other[0, 3] = -math.inf
+        c.put(0, at - 1, v=other)
+        out, _ = c.run(h)
+        assert bool(out[:, :2, 3].isnan().all()) and bool((out[:, :2, 7] == -math.inf).all())
+    assert h.check_device() == 0
