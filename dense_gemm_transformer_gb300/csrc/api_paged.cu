@@ -88,6 +88,7 @@ gemm_status_t check_attention(const gemm_paged_attention_t& a) {
   if ((a.q_token | a.q_head | a.out_token | a.out_head | a.k_page | a.k_slot | a.k_head | a.v_page | a.v_slot |
        a.v_head) % 8 != 0)
     return GEMM_ERR_MISALIGNED;
+  if (a.out == a.q) return GEMM_ERR_INVALID_VALUE;  // rows with results that are not finite are computed again
   return GEMM_OK;
 }
 

@@ -495,6 +495,8 @@ gemm_status_t gemm_rotary(gemm_handle_t h, const gemm_rotary_t* a, void* stream)
  *     s_j = scale * q . k_j, with softcap > 0: softcap * tanh(s_j / softcap)
  *     (a softcap above 2^100 is none)
  *     out = sum_j softmax_j(s) v_j,   lse = log(sum_j exp(s_j))
+ * out must not overlap what is read (out == q is refused): rows may be read
+ * again after others are written.
  * A row that sees no key gives out = 0 and lse = -infinity.  Keys and values
  * that no row sees are not part of any result, whatever they hold.  Scores,
  * softmax and sums are fp32; the softmax weights are rounded to the

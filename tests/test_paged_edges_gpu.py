@@ -334,7 +334,8 @@ def test_a_handle_of_another_device_is_refused(h):
     fake = (ctypes.c_int32 * 4096)(torch.cuda.current_device() + 1)
     handle = ctypes.cast(fake, ctypes.c_void_p)
     assert lib.gemm_rotary(handle, host._pack("gemm_rotary_t", host.ROTARY), None) == host.INVALID
-    assert lib.gemm_paged_attention(handle, host._pack("gemm_paged_attention_t", host.ATTENTION), None) == host.INVALID
+    attention = {**host.ATTENTION, "out": host.P + 0x100000}
+    assert lib.gemm_paged_attention(handle, host._pack("gemm_paged_attention_t", attention), None) == host.INVALID
     c, p = host._cache(), host.P
     assert lib.gemm_cache_grow(handle, c, 1, p, p, 1, p, p, p, None) == host.INVALID
     assert lib.gemm_cache_shrink(handle, c, 1, p, p, None) == host.INVALID
@@ -542,4 +543,28 @@ def test_attention_infinite_values_give_infinities(h, n, length, dtype):
         c.put(0, at - 1, v=other)
         out, _ = c.run(h)
         assert bool(out[:, :2, 3].isnan().all()) and bool((out[:, :2, 7] == -math.inf).all())
+    assert h.check_device() == 0
+
+
+def test_attention_in_place_is_refused(h):
+    """out over q: rows may be computed a second time, from their queries."""
+    c = Case([(40, 100)], 4, 2, 64, 16, BF16)
+    q = c.q.contiguous()
+    with pytest.raises(dg.GemmError, match="INVALID_VALUE"):
+        h.paged_attention(q, c.k, c.v, c.table, c.lens, cu_q=c.cu, max_q=c.max_q, out=q)
+
+
+@pytest.mark.parametrize("lengths", [[(1, 300)], [(100, 300), (1, 20)]])
+def test_attention_broadcast_tensors(h, lengths):
+    """Keys and values of one head expanded to several, queries of one head to several: strides of zero."""
+    c = Case(lengths, 4, 1, 64, 16, BF16, seed=3)
+    q = c.q[:, :1].expand(-1, 4, -1)
+    kw = dict(cu_q=c.cu, max_q=c.max_q, return_lse=True)
+    want = h.paged_attention(q.contiguous(), c.k, c.v, c.table, c.lens, **kw)
+    got = h.paged_attention(q, c.k, c.v, c.table, c.lens, **kw)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    k, v = (t.expand(-1, -1, 4, -1) for t in (c.k, c.v))
+    c.q, c.kv_heads = q, 4
+    c.keys, c.values = [t.expand(-1, 4, -1) for t in c.keys], [t.expand(-1, 4, -1) for t in c.values]
+    c.check(*h.paged_attention(q, k, v, c.table, c.lens, **kw))
     assert h.check_device() == 0

@@ -4,7 +4,7 @@ import torch
 
 import dense_gemm_transformer_gb300 as dg
 from dense_gemm_transformer_gb300 import paged
-from tests.test_paged_host import H, INVALID, MISALIGNED, OK, P, ROTARY, _cache, _pack
+from tests.test_paged_host import ATTENTION, H, INVALID, MISALIGNED, OK, P, ROTARY, _cache, _pack
 
 
 @pytest.fixture(scope="module")
@@ -67,3 +67,9 @@ def test_nothing_to_append_is_no_error(lib):
     assert lib.gemm_rotary(H, _pack("gemm_rotary_t", {**ROTARY, **none}), None) == OK
     assert lib.gemm_rotary(H, _pack("gemm_rotary_t", {**ROTARY, **none, "head_dim": 127}), None) == INVALID
     assert lib.gemm_rotary(H, _pack("gemm_rotary_t", {**ROTARY, **none, "num_pages": -1}), None) == INVALID
+
+
+def test_attention_over_its_queries_is_refused(lib):
+    assert ATTENTION["out"] == ATTENTION["q"]
+    assert lib.gemm_paged_attention(H, _pack("gemm_paged_attention_t", ATTENTION), None) == INVALID
+    assert lib.gemm_paged_attention(H, _pack("gemm_paged_attention_t", {**ATTENTION, "k_slot": 260}), None) == MISALIGNED
