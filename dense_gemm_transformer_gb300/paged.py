@@ -199,16 +199,16 @@ class PagedCache:
         self.page_size = page_size
         self.k = torch.empty((layers, pages, page_size, kv_heads, head_dim), dtype=dtype, device=device)
         self.v = torch.empty_like(self.k)
+        # pages of other than whole 16 bytes cannot be copied: fork refuses them, so none is ever shared
+        self._copied = page_size * kv_heads * head_dim * self.k.element_size() % 16 == 0
         self.table = torch.full((sequences, width), -1, dtype=torch.int32, device=device)
         self.lens = torch.zeros(sequences, dtype=torch.int32, device=device)
         self.refs = torch.zeros(pages, dtype=torch.int32, device=device)
 
     def grow(self, seqs, counts, tokens):
         """cache_grow over every layer: (positions, slots, info) of the new tokens."""
-        # (pages of another size than whole 16 bytes cannot be copied; fork refuses them, so none is ever shared)
-        copied = self.k[0, 0].numel() * self.k.element_size() % 16 == 0 if self.k.numel() else False
         return cache_grow(self.table, self.lens, self.refs, self.page_size, seqs, counts, tokens,
-                          pools=(self.k, self.v) if copied else None)
+                          pools=(self.k, self.v) if self._copied else None)
 
     def shrink(self, seqs, counts=None):
         """cache_shrink: takes tokens back, all of them without counts."""
