@@ -2,6 +2,7 @@
 // argument checks, scratch and launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -79,9 +80,6 @@ gemm_status_t check_attention(const gemm_paged_attention_t& a) {
   if (a.max_q < 1 || a.q == nullptr || a.out == nullptr || a.kv_lens == nullptr) return GEMM_ERR_INVALID_VALUE;
   if (a.table_width > 0 && (a.table == nullptr || (a.num_pages > 0 && (a.k_pages == nullptr || a.v_pages == nullptr))))
     return GEMM_ERR_INVALID_VALUE;
-  // blocks: (sequence, key head, 16 rows) in a 1-D grid
-  const int64_t rows = static_cast<int64_t>(a.max_q) * (a.heads / a.kv_heads);
-  if (static_cast<int64_t>(a.sequences) * a.kv_heads > kMaxInt / ((rows + 15) / 16)) return GEMM_ERR_INVALID_VALUE;
   if (!aligned(a.q, 16) || !aligned(a.out, 16) || !aligned(a.k_pages, 16) || !aligned(a.v_pages, 16) ||
       !aligned(a.table, 4) || !aligned(a.kv_lens, 4) || !aligned(a.cu_q, 4) || !aligned(a.lse, 4))
     return GEMM_ERR_MISALIGNED;
@@ -197,13 +195,20 @@ gemm_status_t gemm_rotary(gemm_handle_t h, const gemm_rotary_t* a, void* stream)
   return cuda_status(dgt::launch_rotary(*a, h->sms, h->d_status, static_cast<cudaStream_t>(stream)));
 }
 
-gemm_status_t gemm_paged_attention(gemm_handle_t h, const gemm_paged_attention_t* a, void* stream) {
-  if (h == nullptr || a == nullptr) return GEMM_ERR_INVALID_VALUE;
-  gemm_status_t st = check_attention(*a);
+gemm_status_t gemm_paged_attention(gemm_handle_t h, const gemm_paged_attention_t* given, void* stream) {
+  if (h == nullptr || given == nullptr) return GEMM_ERR_INVALID_VALUE;
+  gemm_status_t st = check_attention(*given);
   if (st != GEMM_OK) return st;
-  if (a->tokens == 0 || a->sequences == 0) return GEMM_OK;
+  if (given->tokens == 0 || given->sequences == 0) return GEMM_OK;
   st = check_device(h);
   if (st != GEMM_OK) return st;
+  gemm_paged_attention_t bounded = *given;
+  bounded.max_q = static_cast<int32_t>(std::min<int64_t>(bounded.max_q, bounded.tokens));
+  const gemm_paged_attention_t* a = &bounded;
+  // the 16-row kernel's blocks, (sequence, key head, 16 rows), in a 1-D grid
+  const int64_t group = a->heads / a->kv_heads, rows = a->max_q * group;
+  const int64_t row_tiles = ((group <= dgt::kPagedMostGroup ? std::min<int64_t>(rows, dgt::kPagedFewRows) : rows) + 15) / 16;
+  if (static_cast<int64_t>(a->sequences) * a->kv_heads > kMaxInt / row_tiles) return GEMM_ERR_INVALID_VALUE;
   const dgt::PagedPlan plan = dgt::paged_attention_plan(*a, h->sms);
   if (plan.tile_parts > kMaxTileParts) return GEMM_ERR_INVALID_VALUE;
   void* ws;

@@ -52,10 +52,6 @@ constexpr int kStages = 2, kDeepStages = 4;
 constexpr int ring_bytes(int dim, int stages) { return kWarps * stages * 2 * kKeys * dim * 2; }
 // The joins keep the maxima (then weights) and sums of a range's parts there.
 static_assert(kPagedMostSplits * kRows * 2 * static_cast<int>(sizeof(float)) <= ring_bytes(64, kStages));
-// Sequences with more rows a key head go to the tile kernel.  With 30 rows the
-// 16-row one is ahead (10.8 against 14.0 us over 500 keys, 19.5 against 23.7 us
-// in 16 sequences of 2000), with 60 rows behind (28.3 against 24.5 us).
-constexpr int kFewRows = 32;
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool valid) {
   const int bytes = valid ? 16 : 0;  // the rest of the 16 bytes is filled with zeros
@@ -763,8 +759,8 @@ PagedPlan paged_attention_plan(const gemm_paged_attention_t& a, int sms) {
   PagedPlan plan{};
   const int64_t group = a.heads / a.kv_heads;
   const int64_t max_rows = a.max_q * group;
-  plan.tiled = max_rows > kFewRows && group <= 128;
-  const int64_t row_tiles = ((plan.tiled ? kFewRows : max_rows) + kRows - 1) / kRows;
+  plan.tiled = max_rows > kPagedFewRows && group <= kPagedMostGroup;
+  const int64_t row_tiles = ((plan.tiled ? kPagedFewRows : max_rows) + kRows - 1) / kRows;
   const int64_t ranges = static_cast<int64_t>(a.sequences) * a.kv_heads * row_tiles;
   // Parts of a range.  A part more costs the join of a range about 0.1 us
   // and saves every warp of the others a share of its tiles, 1.2 us each: the
@@ -800,9 +796,9 @@ PagedPlan paged_attention_plan(const gemm_paged_attention_t& a, int sms) {
   plan.kernels = 1;
   if (!plan.tiled) return plan;
   // Items of the tile kernel: an upper bound from the call's tokens (a sequence
-  // adds at most one item that is not full, and has more than kFewRows rows).
+  // adds at most one item that is not full, and has more than kPagedFewRows rows).
   const int64_t pair_tokens = 2 * (128 / group);
-  const int64_t long_seqs = std::min<int64_t>(a.sequences, a.tokens * group / (kFewRows + 1));
+  const int64_t long_seqs = std::min<int64_t>(a.sequences, a.tokens * group / (kPagedFewRows + 1));
   const int64_t most = std::max<int64_t>(1, a.kv_heads * (a.tokens / pair_tokens + long_seqs));
   int64_t keys = most_keys(a);
   if (a.window > 0) keys = std::min<int64_t>(keys, a.window + pair_tokens - 1 + 128);
@@ -854,8 +850,8 @@ cudaError_t launch_paged_attention(const gemm_paged_attention_t& a, const PagedP
   p.group = a.heads / a.kv_heads;
   p.group_inv = static_cast<uint32_t>((0x100000000ull + p.group - 1) / p.group);
   p.tiled = plan.tiled;
-  p.few_rows = kFewRows;
-  p.row_tiles = static_cast<int>(((plan.tiled ? kFewRows : static_cast<int64_t>(a.max_q) * p.group) + kRows - 1) / kRows);
+  p.few_rows = kPagedFewRows;
+  p.row_tiles = static_cast<int>(((plan.tiled ? kPagedFewRows : static_cast<int64_t>(a.max_q) * p.group) + kRows - 1) / kRows);
   p.splits = plan.row_splits;
   p.row_stages = plan.row_stages;
   const int64_t tiles = row_key_tiles(a);

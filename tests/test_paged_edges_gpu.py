@@ -568,3 +568,13 @@ def test_attention_broadcast_tensors(h, lengths):
     c.keys, c.values = [t.expand(-1, 4, -1) for t in c.keys], [t.expand(-1, 4, -1) for t in c.values]
     c.check(*h.paged_attention(q, k, v, c.table, c.lens, **kw))
     assert h.check_device() == 0
+
+
+@pytest.mark.parametrize("heads", [8, 258])
+def test_attention_with_a_loose_bound_on_new_tokens(h, heads):
+    """max_q is an upper bound; one far above the tokens there are changes nothing."""
+    c = Case([(1, 30 + i) for i in range(50)] + [(3, 40)], heads, 2, 64, 16, BF16, seed=2)
+    for c.max_q in (100, 2 ** 31 - 1):
+        got = c.run(h)
+        c.check(*got)
+    assert h.check_device() == 0
