@@ -104,6 +104,7 @@ struct RowsShared {
   float f[kWarps][kRows];  // factors of the warps' sums
   float inv[kRows];        // of a joined range: 1 / l
   int last, unit;
+  unsigned redo[kWarps];   // of the items that are looked at: which to compute again
 };
 
 // The sums of a warp that are not numbers though the scores are (lsum: the
@@ -693,31 +694,33 @@ __global__ void __launch_bounds__(kThreads, D == 128 && !TILED ? 3 : 0) paged_ro
     }
     // Items with results that are not finite: a value that a row must not see
     // may have got into it (0 times an infinity), so those rows are computed
-    // again here, where that cannot happen.
-    for (int64_t base = 0; base < parts; base += static_cast<int64_t>(gridDim.x) * kThreads) {
-      const int64_t at = base + static_cast<int64_t>(blockIdx.x) * kThreads;
-      const bool any = at + threadIdx.x < parts &&
-                       reinterpret_cast<const unsigned long long*>(p.redo)[at + threadIdx.x] != 0;
-      if (!__syncthreads_or(any)) continue;
-      for (int64_t idx = at; idx < min(at + kThreads, parts); ++idx) {
-        const unsigned long long flags = reinterpret_cast<const unsigned long long*>(p.redo)[idx];
-        if (flags == 0) continue;
-        const PagedItem it = paged_item(p, static_cast<int>(idx), false);
+    // again here, 16 at a time, where that cannot happen.  The units are dealt
+    // out to the blocks one by one.
+    const int64_t units = parts * 16, grid = gridDim.x;
+    for (int64_t base = blockIdx.x; base < units; base += grid * kThreads) {
+      const int64_t mine = base + threadIdx.x * grid;
+      const unsigned flagged = __ballot_sync(0xffffffffu, mine < units && p.redo[mine / 2] != 0);
+      if ((threadIdx.x & 31) == 0) sh.redo[threadIdx.x / 32] = flagged;
+      if (!__syncthreads_or(flagged != 0)) continue;
+      for (int t = 0; t < kThreads; ++t) {
+        if ((sh.redo[t / 32] >> (t % 32) & 1) == 0) continue;
+        const int64_t u = base + t * grid;
+        const int w = static_cast<int>(u % 16) / 2, half = static_cast<int>(u % 2);
+        const PagedItem it = paged_item(p, static_cast<int>(u / 16), false);
         if (!it.valid) break;
-        for (int w = 0; w < 8; ++w) {
-          if (((flags >> (8 * w)) & 0xff) == 0) continue;
-          const int tile_rows = p.tile_tokens * p.group;
-          const int tile0 = (2 * it.pair + w / 4) * tile_rows;
-          const int64_t end = min(static_cast<int64_t>(tile0) + tile_rows, static_cast<int64_t>(it.s.n) * p.group);
-          for (int half = 0; half < 2; ++half) {
-            const int row0 = tile0 + (w % 4) * 32 + half * kRows;
-            if (row0 >= end) continue;
-            __syncthreads();  // the shared memory of the rows before
-            rows_unit<T, D>(p, smem, sh, it.s, it.seq, it.head, row0,
-                            static_cast<int>(min(end - row0, static_cast<int64_t>(kRows))), 0, 1, 0, -1, 0);
-          }
-        }
+        // the same rows' other parts: the first one that is flagged has them done
+        bool done = false;
+        for (int q = 1; q <= it.split; ++q) done |= p.redo[(it.part - q) * static_cast<int64_t>(8) + w] != 0;
+        const int tile_rows = p.tile_tokens * p.group;
+        const int tile0 = (2 * it.pair + w / 4) * tile_rows;
+        const int64_t end = min(static_cast<int64_t>(tile0) + tile_rows, static_cast<int64_t>(it.s.n) * p.group);
+        const int row0 = tile0 + (w % 4) * 32 + half * kRows;
+        if (done || row0 >= end) continue;
+        __syncthreads();  // the shared memory of the rows before
+        rows_unit<T, D>(p, smem, sh, it.s, it.seq, it.head, row0,
+                        static_cast<int>(min(end - row0, static_cast<int64_t>(kRows))), 0, 1, 0, -1, 0);
       }
+      __syncthreads();  // sh.redo is written again
     }
   }
 }
