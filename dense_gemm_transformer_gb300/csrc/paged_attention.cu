@@ -111,41 +111,51 @@ struct RowsShared {
 // rows' sums of weights): a value that a row sees is infinite or not a number.
 // Of a weight's two 16-bit numbers one may be 0 or negative, and the sum of
 // their products with an infinity NaN; which infinity it should be is found
-// from the values.  Not inlined: its registers are the kernel's otherwise, and
-// those decide how many blocks an SM has.
+// from the values, a tile at a time for all rows.  Not inlined: its registers
+// are the kernel's otherwise, and those decide how many blocks an SM has.
 template <typename T, int D>
 __device__ __noinline__ void infinite_sums(const PagedParams& p, float* sums, const float* lsum, const int32_t* table,
                                            const T* vbase, int rows, int head0, int seen0, int tile, int tiles) {
+  constexpr int kCols = D / 32;  // a lane's columns, consecutive ones
+  struct alignas(2 * kCols) Cols {
+    T x[kCols];
+  };
   const gemm_paged_attention_t& a = p.a;
   const int lane = threadIdx.x & 31;
+  // row `lane` sees the keys [from, to)
+  const int to = lane < rows ? max(0, seen0 + by_group(p, head0 + lane)) : 0;
+  const int from = a.window > 0 ? max(0, to - a.window) : 0;
+  unsigned plus[kCols] = {}, minus[kCols] = {}, nan[kCols] = {};  // bit r: row r sees such a value
+#pragma unroll 1
+  for (int it = 0; it < tiles; ++it) {
+    const int key0 = (tile + it * kWarps) * kKeys, col = key0 / a.page_size;
+    const int page = table[col];
+    if (page < 0 || page >= a.num_pages) continue;
+    const T* v = vbase + page * a.v_page + (key0 - col * a.page_size) * a.v_slot + kCols * lane;
+    Cols y[kKeys];
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k) y[k] = *reinterpret_cast<const Cols*>(v + k * a.v_slot);
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k) {
+      const unsigned seen = __ballot_sync(0xffffffffu, key0 + k >= from && key0 + k < to);
+#pragma unroll
+      for (int x = 0; x < kCols; ++x) {
+        const float f = as_f(y[k].x[x]);
+        plus[x] |= f == -neg_inf() ? seen : 0u;
+        minus[x] |= f == neg_inf() ? seen : 0u;
+        nan[x] |= isnan(f) ? seen : 0u;
+      }
+    }
+  }
 #pragma unroll 1
   for (int r = 0; r < rows; ++r) {
-    float* row = sums + r * D;
-    const int swap = 8 * (r & 3);
-    bool open = false;
+    if (isnan(lsum[r])) continue;  // scores that are not numbers leave no other result
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) open |= isnan(row[(32 * x + lane) ^ swap]);
-    if (!__any_sync(0xffffffffu, open) || isnan(lsum[r])) continue;
-    const int to = max(0, seen0 + by_group(p, head0 + r)), from = a.window > 0 ? max(0, to - a.window) : 0;
-    int kinds[D / 32] = {};  // 1: infinity, 2: minus infinity, 4: not a number
-#pragma unroll 1
-    for (int it = 0; it < tiles; ++it) {
-      const int key0 = (tile + it * kWarps) * kKeys, col = key0 / a.page_size;
-      if (key0 + kKeys <= from || key0 >= to) continue;
-      const int page = table[col];
-      if (page < 0 || page >= a.num_pages) continue;
-      const T* v = vbase + page * a.v_page + (key0 - col * a.page_size) * a.v_slot + lane;
-#pragma unroll 1
-      for (int key = max(key0, from); key < min(key0 + kKeys, to); ++key)
-#pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          const float y = as_f(v[(key - key0) * a.v_slot + 32 * x]);
-          if (!isfinite(y)) kinds[x] |= isnan(y) ? 4 : y > 0.f ? 1 : 2;
-        }
+    for (int x = 0; x < kCols; ++x) {
+      float* at = sums + r * D + ((kCols * lane + x) ^ (8 * (r & 3)));
+      const bool up = plus[x] >> r & 1, down = minus[x] >> r & 1;
+      if (isnan(*at) && up != down && !(nan[x] >> r & 1)) *at = up ? -neg_inf() : neg_inf();
     }
-#pragma unroll
-    for (int x = 0; x < D / 32; ++x)
-      if (kinds[x] == 1 || kinds[x] == 2) row[(32 * x + lane) ^ swap] = kinds[x] == 1 ? -neg_inf() : neg_inf();
   }
 }
 

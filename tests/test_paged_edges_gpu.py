@@ -578,3 +578,28 @@ def test_attention_with_a_loose_bound_on_new_tokens(h, heads):
         got = c.run(h)
         c.check(*got)
     assert h.check_device() == 0
+
+
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+@pytest.mark.parametrize("lengths", [[(512, 4096)], [(1, 4096)] * 16])
+def test_attention_time_with_values_that_are_not_finite(h, lengths, bad):
+    """A value of every head that every row sees: all rows are computed again, which takes longer, not forever."""
+    c = Case(lengths, 32, 4, 128, 64, BF16, seed=17)
+
+    def time():
+        c.run(h)
+        began, ended = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        began.record()
+        c.run(h)
+        ended.record()
+        torch.cuda.synchronize()
+        return began.elapsed_time(ended)
+
+    clean = min(time() for _ in range(3))
+    for b in range(len(lengths)):
+        c.put(b, 100, v=torch.full((4, 128), bad))
+    out, lse = c.run(h)
+    assert bool((out.isnan() if bad != bad else out == math.inf).all()) and bool(torch.isfinite(lse).all())
+    spent = min(time() for _ in range(3))
+    assert spent < 100 * clean + 1.0, (spent, clean)
+    assert h.check_device() == 0
