@@ -7,9 +7,10 @@
 // whose blocks each list the free (and used) pages of a segment of `refs`;
 // the block that finishes last has every segment's counts, and does the rest
 // of the call alone, so that a decode step costs one launch.  Moving the
-// pages' bytes is a second kernel that reads how many there are on the
-// device; it is bound by HBM, 2 x the bytes: 794 MB of reads and writes take
-// 137 us with the ranks before them, 5.8 TB/s.
+// pages' bytes (a fork's last pages, compaction, a page that a growing sequence
+// shares) is a second kernel that reads how many there are on the device; it is
+// bound by HBM, 2 x the bytes: 794 MB of reads and writes take 137 us with the
+// ranks before them, 5.8 TB/s.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -9,9 +9,9 @@
 // modulo a turn before it becomes a float: f_i / 2 pi as a 64-bit fraction
 // of a turn (one multiplication in double precision a frequency, rounded to
 // 2^-53 of itself), times the position in integer arithmetic, which wraps at
-// whole turns by itself and so is exact for every position.  The fp32
-// product position * f_i would be off by position * f_i * 2^-24: a tenth of
-// a turn near position 10^6.
+// whole turns by itself and adds no error of its own at any position.  The
+// fp32 product position * f_i would be off by position * f_i * 2^-24: a tenth
+// of a turn near position 10^6.
 //
 // The kernel reads and writes each element once and is bound by that
 // traffic.  A block has a few tokens: its threads compute their sines and

@@ -447,8 +447,10 @@ typedef enum {
  * the gradient of (a', b') to that of (a, b).  Pair i is elements (2 i,
  * 2 i + 1) when interleaved = 1, (i, i + rotary_dim / 2) otherwise; elements
  * from rotary_dim on are copied.  The angle is reduced to a turn in 64-bit
- * fixed point, exact for any position; arithmetic in fp32, one rounding to
- * out_type at the end.
+ * fixed point: it is off by what rounding freqs[i] / 2 pi to 53 bits, and to
+ * 2^-64 of a turn, makes of it, |positions[t]| (2^-52 |freqs[i]| + 2^-61)
+ * radians, besides the 2^-24 of half a turn of an fp32 number.  Arithmetic in
+ * fp32, one rounding to out_type at the end.
  *
  * page_size == 0: q (heads) and, unless k is NULL, k (kv_heads) go to q_out
  * and k_out; v must be NULL.  In place (q_out == q, k_out == k with equal
@@ -498,10 +500,15 @@ gemm_status_t gemm_rotary(gemm_handle_t h, const gemm_rotary_t* a, void* stream)
  * out must not overlap what is read (out == q is refused): rows may be read
  * again after others are written.
  * A row that sees no key gives out = 0 and lse = -infinity.  Keys and values
- * that no row sees are not part of any result, whatever they hold.  Scores,
- * softmax and sums are fp32; the softmax weights are rounded to the
- * operands' type (to twice its significant bits for at most 16 rows a key
- * head) for the product with the values. */
+ * that a row does not see are no part of its result, whatever they hold.  An
+ * infinity or NaN among the values that a chunk's tiles read makes those rows
+ * be computed a second time, 16 at a time: some twenty times as long where that
+ * is all of them.  Scores, softmax and sums are fp32 (the tensor cores round
+ * their sums toward zero: up to 2^-24 of the sum for every 16 keys); the
+ * softmax weights are rounded to the operands' type for the product with the
+ * values, to twice its significant bits in sequences with at most 32 rows a key
+ * head (new tokens times heads a key head) and where heads / kv_heads is above
+ * 128. */
 typedef struct {
   int32_t type;                /* GEMM_TYPE_BF16 or GEMM_TYPE_FP16: q, pages, out  */
   int32_t sequences, heads, kv_heads;
