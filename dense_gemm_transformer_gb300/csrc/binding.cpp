@@ -83,7 +83,7 @@ gemm_handle_t handle_of(PyObject* o) {  // None: a closed handle, which the libr
 
 // A stream as it is given: a torch stream or a raw handle.
 void* stream_of(PyObject* given) {
-  if (PyLong_Check(given)) return PyLong_AsLongLong(given) == 0 ? nullptr : address(given);
+  if (PyLong_Check(given)) return address(given);
   PyObject* raw = PyObject_GetAttrString(given, "cuda_stream");
   if (raw == nullptr) throw Raised{};
   void* s = PyLong_AsVoidPtr(raw);
@@ -92,13 +92,20 @@ void* stream_of(PyObject* given) {
   return s;
 }
 
+// The current device, -1 where there is none.
+c10::DeviceIndex current_device() {
+  c10::DeviceIndex current = -1;
+  return c10::cuda::GetDevice(&current) == cudaSuccess ? current : static_cast<c10::DeviceIndex>(-1);
+}
+
 // While it lives, new tensors come from the memory of the call's stream, as
 // under torch.cuda.stream: a block of the current stream's could still be in
 // use by work that the call's stream does not wait for.
 class OutputsOn {
  public:
   OutputsOn(PyObject* given, const at::Tensor& like) {
-    if (given == Py_None || !like.is_cuda()) return;  // (another device's tensor is refused below)
+    // (a tensor of another device is refused by Device::on)
+    if (given == Py_None || !like.is_cuda() || like.get_device() != current_device()) return;
     const c10::DeviceIndex device = like.get_device();
     void* raw = stream_of(given);
     current_ = c10::cuda::getCurrentCUDAStream(device);
@@ -126,10 +133,8 @@ struct Device {
   void on(const at::Tensor& t, const char* name) {
     if (!t.is_cuda()) refuse(std::string(name) + " must be a CUDA tensor");
     if (index < 0) {
-      c10::DeviceIndex current = -1;
-      if (c10::cuda::GetDevice(&current) != cudaSuccess) current = -1;
       index = t.get_device();
-      if (index != current) refuse(std::string(name) + " must be on the current device");
+      if (index != current_device()) refuse(std::string(name) + " must be on the current device");
     }
     if (t.get_device() != index) refuse("all tensors must be on one device");
   }

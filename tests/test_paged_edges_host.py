@@ -46,6 +46,8 @@ def test_tensors_of_another_device_are_refused(lib):
     with pytest.raises(ValueError, match="current device"):
         ops.rotary(x, None, slots, slots, q_out=x)
     with pytest.raises(ValueError, match="current device"):
+        ops.rotary(x, None, slots, slots, q_out=x, stream=0x1000)
+    with pytest.raises(ValueError, match="current device"):
         ops.rotary_append(x, x, x, None, slots, pages, pages, q_out=x)
     with pytest.raises(ValueError, match="current device"):
         ops.paged_attention(x, pages, pages, table, lens, out=x)
