@@ -21,8 +21,8 @@
 // there are too few (sequence, head) pairs to fill the SMs; the block that
 // finishes last joins the parts, in the parts' order, so the result does not
 // depend on which one that is.  One token in each of 64 sequences of 1 to 8192
-// keys, 12 heads of 128 over 2: 63 us, 4.8 TB/s; against 1001 keys of one
-// sequence 8.6 us, a chain of latencies.
+// keys, 12 heads of 128 over 2: 63 us, 4.7 TB/s; against 1001 keys of one
+// sequence 8.5 us, a chain of latencies.
 //
 // A tile that some row of the block sees only in part goes without the
 // matrix instruction for the values: there, 0 x v would let an infinity or

@@ -29,7 +29,7 @@
 //               until then the weights stay below 2^kSlack, which neither
 //               their 16-bit form nor the fp32 sums lose accuracy by.
 //
-// A prompt of 8192 tokens, 64 heads of 128, takes 820 us (1.34 PFLOP/s, at the
+// A prompt of 8192 tokens, 64 heads of 128, takes 830 us (1.32 PFLOP/s, at the
 // card's power limit).
 //
 // Slots past the sequence's last token may hold anything: their scores are
@@ -131,7 +131,7 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // Four scores share one reciprocal, that of their product (1 / u = r v for
 // r = 1 / (u v)): reciprocals run at half the rate of exponentials here, and
 // one each made a chunk of 512 tokens, 64 heads, against 8192 keys 190 us, one
-// for two 173, one for four 166 (175 with the mask before them, which this
+// for two 173, one for four 166 (172 with the mask before them, which this
 // needs).  The exponents stop at 30, where 1/2 - 1 / (2^30 + 1) is 1/2 in fp32,
 // so that the product stays finite.  A NaN that a row sees makes all of its
 // outputs NaN with or without that.
